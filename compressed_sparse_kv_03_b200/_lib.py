@@ -25,6 +25,8 @@ KERNEL_MERGE = 3
 KERNEL_COMPRESS = 4
 KERNEL_QUANTIZE = 5
 KERNEL_TOPK_SAMPLE = 6
+KERNEL_KV_APPEND = 7
+KERNEL_KV_EVICT = 8
 
 
 class CsaError(RuntimeError):
@@ -45,8 +47,24 @@ class QRopeT(C.Structure):
                 ("rope_base", C.c_float), ("derotate", C.c_int32), ("pos", C.c_void_p)]
 
 
+class KvCacheT(C.Structure):
+    """Mirror of csa_kv_cache_t."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("n_pages", C.c_int64),
+                ("k_page_stride", C.c_int64), ("k_slot_stride", C.c_int64), ("k_head_stride", C.c_int64),
+                ("v_page_stride", C.c_int64), ("v_slot_stride", C.c_int64), ("v_head_stride", C.c_int64),
+                ("page_table", C.c_void_p), ("max_pages", C.c_int32), ("page_size", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("dtype", C.c_int32)]
+
+
+class KvRowsT(C.Structure):
+    """Mirror of csa_kv_rows_t."""
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
 _vp, _i32, _i64, _f32, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_size_t
 _qr = C.POINTER(QRopeT)
+_kv = C.POINTER(KvCacheT)
+_rows = C.POINTER(KvRowsT)
 
 # name -> (restype, argtypes); the exact list of functions include/csa.h declares
 SIGNATURES = {
@@ -86,6 +104,14 @@ SIGNATURES = {
     "csa_sparse_attn_decode_noalloc": (C.c_int, [_vp, C.POINTER(CacheT), _vp, _vp, _vp, _vp, _i32,
                                                  _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp,
                                                  _vp]),
+    "csa_kv_append": (C.c_int, [_rows, _rows, _kv, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp,
+                                _sz, _vp]),
+    "csa_kv_attn_decode_workspace_size": (_sz, [_i32, _i32, _kv, _i64, _i32]),
+    "csa_kv_attn_decode": (C.c_int, [_rows, _kv, _vp, _i32, _i32, _i64, _i32, _f32, _vp, _vp, _vp, _vp,
+                                     _vp, _i64, _vp, _sz, _vp]),
+    "csa_kv_evict_workspace_size": (_sz, [_i32, _i32, _i32, _i64]),
+    "csa_kv_evict": (C.c_int, [_kv, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _i32, _i32, _i32,
+                               _i64, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None

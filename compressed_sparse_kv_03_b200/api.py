@@ -13,9 +13,17 @@ the current torch stream.  Shapes follow the header:
     sparse_attn_decode   (step 4)    q [B, H, d] over cache[idx] + window buffer
     hca_attn             (step 4)    q [T, H, d] over all eligible entries + window
                                      (d = 128, or 512: the pages' entry width)
+
+Per-head key-value caches (KVCache: ordinary multi-head / grouped-query attention,
+or a shared-KV cache with k is v):
+
+    kv_append            new tokens' k, v [T, H_kv, d] -> the cache, behind each sequence's last slot
+    kv_attn_decode       q [B, H, d] over every slot, optionally adding each slot's attention weight up
+    kv_evict             cut sequences to a budget of slots, per head, by accumulated weight
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from dataclasses import dataclass
 from typing import Optional
@@ -23,7 +31,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import CacheT, QRopeT, check, load
+from ._lib import CacheT, KvCacheT, KvRowsT, QRopeT, check, load
 
 
 def _ptr(t):
@@ -486,6 +494,230 @@ def hca_attn(q, kv: Cache, kv_win, m, window, sm_scale, *, win_len=None, q_pos=N
                        max_entries, window, float(sm_scale), _ptr(sink), _ptr(out), _ptr(lse), wsp,
                        wsb, _stream(stream), _qrope_c(qrope, dev)))
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# per-head key-value caches
+# ---------------------------------------------------------------------------
+_KV_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+class KVCache:
+    """A per-head key-value cache: k and v [n_pages, page_size, H_kv, d] (bf16 or
+    fp16; any strides that are multiples of 8 with the last dimension
+    contiguous, so head-major storage and interleaved keys and values are
+    views), with page_table [n_seq, max_pages] int32, or without one: sequence
+    b is page b.  k and v may be one tensor (shared KV).  Holds the tensors;
+    the struct passed to the library is made once."""
+
+    def __init__(self, k, v, page_table=None):
+        for name, t in (("k", k), ("v", v)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype not in _KV_DTYPES:
+                raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be [n_pages, page_size, heads, d], got {tuple(t.shape)}")
+            if t.stride(3) != 1 and t.shape[3] > 1:
+                raise ValueError(f"{name}: the last dimension must be contiguous")
+        if v.dtype != k.dtype or v.shape != k.shape or v.device != k.device:
+            raise ValueError("k and v must have one dtype, shape and device")
+        if page_table is not None:
+            _need(page_table, "page_table", torch.int32, 2, k.device)
+        self.k, self.v, self.page_table = k, v, page_table
+        self.device, self.dtype = k.device, k.dtype
+        n_pages, self.page_size, self.n_kv_heads, self.head_dim = k.shape
+        self.max_pages = 1 if page_table is None else page_table.shape[1]
+        self.capacity = self.max_pages * self.page_size
+        self.n_seq = n_pages if page_table is None else page_table.shape[0]
+        # a dimension of one element is never stepped over: its stride says nothing
+        st = [s if n > 1 else 0 for t in (k, v) for n, s in zip(t.shape[:3], t.stride()[:3])]
+        self._c = KvCacheT(k.data_ptr(), v.data_ptr(), n_pages, *st,
+                           None if page_table is None else page_table.data_ptr(), self.max_pages,
+                           self.page_size, self.n_kv_heads, self.head_dim, _KV_DTYPES[k.dtype])
+        self._ref = C.byref(self._c)
+
+    @staticmethod
+    def new(n_seq, max_len, n_kv_heads, head_dim, dtype=torch.bfloat16, device="cuda"):
+        """A zeroed contiguous cache of max_len slots per sequence."""
+        shape = (n_seq, max_len, n_kv_heads, head_dim)
+        return KVCache(torch.zeros(shape, dtype=dtype, device=device),
+                       torch.zeros(shape, dtype=dtype, device=device))
+
+
+def _kv_rows(t, name, cache, heads=None):
+    if t.dtype is not cache.dtype or t.device != cache.device:
+        raise TypeError(f"{name} must be {cache.dtype} on {cache.device}, got {t.dtype} on {t.device}")
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {'H' if heads is None else heads}, {cache.head_dim}], "
+                         f"got {tuple(t.shape)}")
+    n, h, d = t.shape
+    ts, hs, es = t.stride()
+    if es != 1 and d > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return C.byref(KvRowsT(t.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0))
+
+
+def _kv_array(t, name, dtype, B, cache, slots=None):
+    """A [B] or [B, H_kv, slots] array beside the cache; returns its pointer."""
+    shape = (B,) if slots is None else (B, cache.n_kv_heads, slots)
+    if t.dtype is not dtype or t.device != cache.device:
+        raise TypeError(f"{name} must be {dtype} on {cache.device}, got {t.dtype} on {t.device}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+_kv_ws = {}
+
+
+def _kv_scratch(ws, dev, stream, nbytes):
+    """Scratch of a call without a workspace of its own: one buffer per device
+    and stream, so that calls on two streams never share one; inside a stream
+    capture a buffer from the capture's own pool."""
+    if ws is None:
+        if torch.cuda.is_current_stream_capturing():
+            ws = Workspace(dev)
+        else:
+            key = (dev.index, stream.cuda_stream)
+            ws = _kv_ws.get(key)
+            if ws is None:
+                ws = _kv_ws[key] = Workspace(dev)
+    return ws.get(nbytes)
+
+
+@contextlib.contextmanager
+def _on(dev, stream):
+    """Run on `dev` and on `stream` (default: that device's current stream), so
+    that launches and allocations belong there."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream(dev)
+        else:
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def kv_append(k_new, v_new, cache: KVCache, lens, *, token_start=None, pos=None, weights=None,
+              slot_pos=None, lens_out=None, ws=None, stream=None):
+    """Write new tokens' keys and values [T, H_kv, d] behind each sequence's last
+    slot and return the new lengths (`lens` updated in place unless lens_out is
+    given).  token_start [B + 1] int32: sequence b's tokens are rows
+    token_start[b] .. token_start[b+1]-1; without it one token per sequence.
+    `weights` and `slot_pos` [B, H_kv, slots], the state kv_evict goes by, get 0
+    and the token's position (from pos [B], that of each sequence's first new
+    token) at the new slots."""
+    B = lens.shape[0]
+    T = k_new.shape[0]
+    if v_new.shape[0] != T:
+        raise ValueError("k_new and v_new differ in length")
+    if B > cache.n_seq:
+        raise ValueError(f"{B} sequences, but the cache has {cache.n_seq}")
+    kr = _kv_rows(k_new, "k_new", cache, cache.n_kv_heads)
+    vr = _kv_rows(v_new, "v_new", cache, cache.n_kv_heads)
+    lp = _kv_array(lens, "lens", torch.int32, B, cache)
+    if lens_out is None:
+        lens_out = lens
+    op = _kv_array(lens_out, "lens_out", torch.int32, B, cache)
+    if token_start is not None:
+        _need(token_start, "token_start", torch.int32, 1, cache.device)
+        if token_start.shape[0] != B + 1:
+            raise ValueError("token_start must be [B + 1]")
+    slots = 0
+    wp = sp = pp = None
+    if weights is not None or slot_pos is not None:
+        slots = (weights if weights is not None else slot_pos).shape[-1]
+        if weights is not None:
+            wp = _kv_array(weights, "weights", torch.float32, B, cache, slots)
+        if slot_pos is not None:
+            sp = _kv_array(slot_pos, "slot_pos", torch.int32, B, cache, slots)
+    if pos is not None:
+        pp = _kv_array(pos, "pos", torch.int32, B, cache)
+    with _on(cache.device, stream) as s:
+        wsp, wsb = _kv_scratch(ws, cache.device, s, 256)
+        check(load().csa_kv_append(kr, vr, cache._ref, _ptr(token_start), T, B, lp, op, pp, wp, sp, slots,
+                                   wsp, wsb, s.cuda_stream))
+    return lens_out
+
+
+def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0, sink=None,
+                   weights=None, weights_out=None, return_lse=False, ws=None, stream=None, out=None):
+    """Attention of one token per sequence, q [B, H, d], over slots
+    0 .. lens[b]-1 of its sequence (or the last `window` of them); H a multiple
+    of the cache's heads, whose groups of query heads share a KV head.  max_len
+    bounds the lengths (default: the cache's capacity).  With weights_out
+    [B, H_kv, slots] fp32 every slot's probability, summed over the group, is
+    added to weights (default: to zero) and stored there; `weights` alone is
+    updated in place."""
+    B, H = q.shape[0], q.shape[1]
+    if B > cache.n_seq:
+        raise ValueError(f"{B} sequences, but the cache has {cache.n_seq}")
+    qr = _kv_rows(q, "q", cache)
+    lp = _kv_array(lens, "lens", torch.int32, B, cache)
+    if max_len is None:
+        max_len = cache.capacity
+    slots = 0
+    wp = op = None
+    if weights is not None and weights_out is None:
+        weights_out = weights
+    if weights_out is not None:
+        slots = weights_out.shape[-1]
+        op = _kv_array(weights_out, "weights_out", torch.float32, B, cache, slots)
+        if weights is not None:
+            wp = _kv_array(weights, "weights", torch.float32, B, cache, slots)
+    if sink is not None:
+        _need(sink, "sink", torch.float32, 1, cache.device)
+        if sink.shape[0] != H:
+            raise ValueError("sink must be [H]")
+    lib = load()
+    with _on(cache.device, stream) as s:
+        if out is None:
+            out = torch.empty((B, H, cache.head_dim), dtype=cache.dtype, device=cache.device)
+        elif out.dtype is not cache.dtype or out.device != cache.device or out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous, with the shape and dtype of q")
+        lse = torch.empty((B, H), dtype=torch.float32, device=cache.device) if return_lse else None
+        need = lib.csa_kv_attn_decode_workspace_size(B, H, cache._ref, max_len, 0 if op is None else 1)
+        wsp, wsb = _kv_scratch(ws, cache.device, s, need)
+        check(lib.csa_kv_attn_decode(qr, cache._ref, lp, B, H, max_len, window, sm_scale, _ptr(sink),
+                                     out.data_ptr(), _ptr(lse), wp, op, slots, wsp, wsb, s.cuda_stream))
+    return (out, lse) if return_lse else out
+
+
+def kv_evict(cache: KVCache, lens, weights, slot_pos, pos, budget, recent, *, keep_first=0,
+             max_len=None, lens_out=None, weights_out=None, slot_pos_out=None, return_src=False,
+             ws=None, stream=None):
+    """Cut every sequence longer than `budget` slots down to it, per KV head: the
+    slots of the last `recent` positions (pos [B] is the newest one) and of the
+    first `keep_first` stay, then those with the most accumulated weight; a
+    staying slot above the budget moves, with its row, weight and position, into
+    one below it that did not stay.  Everything is updated in place unless
+    *_out arrays are given.  Returns the new lengths, and with return_src the
+    slot [B, H_kv, budget] int32 that each slot's row came from (-1: none)."""
+    B, slots = lens.shape[0], weights.shape[-1]
+    if B > cache.n_seq:
+        raise ValueError(f"{B} sequences, but the cache has {cache.n_seq}")
+    lens_out = lens if lens_out is None else lens_out
+    weights_out = weights if weights_out is None else weights_out
+    slot_pos_out = slot_pos if slot_pos_out is None else slot_pos_out
+    if max_len is None:
+        max_len = min(slots, cache.capacity)
+    args = (_kv_array(lens, "lens", torch.int32, B, cache),
+            _kv_array(lens_out, "lens_out", torch.int32, B, cache),
+            _kv_array(weights, "weights", torch.float32, B, cache, slots),
+            _kv_array(weights_out, "weights_out", torch.float32, B, cache, slots),
+            _kv_array(slot_pos, "slot_pos", torch.int32, B, cache, slots),
+            _kv_array(slot_pos_out, "slot_pos_out", torch.int32, B, cache, slots), slots,
+            _kv_array(pos, "pos", torch.int32, B, cache))
+    lib = load()
+    with _on(cache.device, stream) as s:
+        src = torch.empty((B, cache.n_kv_heads, max(0, budget)), dtype=torch.int32, device=cache.device) if return_src else None
+        wsp, wsb = _kv_scratch(ws, cache.device, s,
+                               lib.csa_kv_evict_workspace_size(B, cache.n_kv_heads, budget, max_len))
+        check(lib.csa_kv_evict(cache._ref, *args, B, budget, recent, keep_first, max_len, _ptr(src), wsp, wsb,
+                               s.cuda_stream))
+    return (lens_out, src) if return_src else lens_out
 
 
 def launch_count():

@@ -216,6 +216,8 @@ void record_event(cudaEvent_t ev, cudaStream_t stream) {
 
 void set_last_error(const char* msg) { g_last_error = msg; }
 
+bool batch_invariant() { return g_batch_invariant.load(std::memory_order_relaxed) != 0; }
+
 int32_t attention_kernel_choice() { return g_attn_kernel.load(std::memory_order_relaxed); }
 
 bool take_attention_timeout_test() { return g_timeout_test.exchange(0, std::memory_order_relaxed) != 0; }
@@ -316,8 +318,10 @@ csa_status_t csa_workspace_check(void* ws, csa_stream_t stream) {
                                 "page id outside the pool", "eligible entries above max_entries",
                                 "window length outside [0, window]",
                                 "a bounded pipeline wait timed out",
-                                "top-k scratch inconsistent"};
-  const char* what = (h.code > 0 && h.code <= 6) ? names[h.code] : "unknown";
+                                "top-k scratch inconsistent",
+                                "sequence length outside [0, max_len]",
+                                "no room for a token"};
+  const char* what = (h.code > 0 && h.code <= 8) ? names[h.code] : "unknown";
   fail(CSA_ERR_DEVICE_CHECK, "device check: %s (query %d, value %lld)", what, h.where,
        (long long)h.value);
   e = cudaMemsetAsync(ws, 0, kWsHeader, (cudaStream_t)stream);

@@ -29,6 +29,8 @@ enum DevErr : int32_t {
   kErrWindow = 4,        // window length outside [0, window]
   kErrTimeout = 5,       // a bounded wait on a pipeline barrier gave up
   kErrSelect = 6,        // top-k scratch inconsistent (histogram below k)
+  kErrLength = 7,        // sequence length outside [0, max_len]
+  kErrRoom = 8,          // no slot left for an appended token
 };
 
 __device__ __forceinline__ void report(WsHeader* h, int32_t code, int32_t where, int64_t value) {

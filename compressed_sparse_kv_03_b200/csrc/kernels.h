@@ -4,6 +4,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "kv.cuh"
 
 namespace csa {
 
@@ -15,7 +16,9 @@ enum KernelId : int32_t {
   kKernelCompress = 4,
   kKernelQuantize = 5,
   kKernelTopkSample = 6,   // the fused selection's sampling / threshold pass
-  kNumKernelIds = 7,
+  kKernelKvAppend = 7,
+  kKernelKvEvict = 8,
+  kNumKernelIds = 9,
 };
 
 // Per-call launch context: the stream plus the timing / launch-count hooks.
@@ -358,6 +361,91 @@ inline cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, si
   }
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
+
+// ---- per-head key-value caches (byte strides throughout) ----
+struct KvAppendArgs {
+  KvRef kv;
+  const char *k_new, *v_new;
+  int64_t k_token, k_head, v_token, v_head;
+  const int32_t* token_start;   // [B+1] or null: one token per sequence
+  int64_t n_tokens;
+  int32_t B, n_kv_heads, chunks;   // chunks: 16-byte pieces of a head's row
+  const int32_t* lens;
+  int32_t* lens_out;
+  const int32_t* pos;
+  float* weights;
+  int32_t* slot_pos;
+  int64_t slots;                // 0: neither weights nor slot_pos
+  WsHeader* err;
+};
+cudaError_t launch_kv_append(const Launch& L, const KvAppendArgs& a);
+
+struct KvEvictArgs {
+  KvRef kv;
+  int32_t B, n_kv_heads, chunks;
+  const int32_t* lens;
+  int32_t* lens_out;
+  const float* weights;
+  float* weights_out;
+  const int32_t* slot_pos;
+  int32_t* slot_pos_out;
+  int64_t slots;
+  const int32_t* pos;
+  int32_t budget, recent, keep_first;
+  int64_t max_len;
+  int32_t* src_out;
+  int32_t* list;                // [B * n_kv_heads][2][list_len]: holes, then the slots that fill them
+  int64_t list_len;
+  int32_t shared;               // 1: keys and values are the same memory
+  int32_t key_cap;              // keys a CTA holds in shared memory (set by the launch)
+  WsHeader* err;
+};
+cudaError_t launch_kv_evict(const Launch& L, const KvEvictArgs& a);
+
+struct KvAttnArgs {
+  KvRef kv;
+  const char* q;
+  int64_t q_token, q_head;
+  int32_t B, H, n_kv_heads, d;
+  int32_t dtype;                // csa_kv_dtype_t
+  const int32_t* lens;
+  int64_t max_len;
+  int32_t window;
+  float scale;                  // sm_scale * log2(e)
+  const float* sink;
+  char* out;                    // [B, H, d]
+  float* lse;
+  const float* weights;
+  float* weights_out;
+  int64_t slots;
+  // scratch
+  float* part_acc;              // [pieces][heads of a unit][padded d]
+  float* part_ml;               // [pieces][heads of a unit][2]
+  float* lse2;                  // [B, H] log2 of the denominators (weights_out only)
+  float* scores;                // [B, H, score_stride] scaled scores, base 2 (weights_out only)
+  int64_t score_stride;
+  int32_t n_ctas;               // CTAs that share the tiles
+  int32_t whole;                // 1: one CTA per unit, nothing to join
+  int32_t atom;                 // tiles that stay together (batch-invariant: a slice)
+  int32_t invariant;
+  int64_t max_atoms;            // slices of a unit of max_len slots (invariant)
+  WsHeader* err;
+};
+// Geometry of a call, shared by the workspace size and the launch.
+struct KvAttnPlan {
+  int wh;                       // 16-head warps side by side in a CTA
+  int blocks;                   // head blocks of a group
+  int dp;                       // padded head dim
+  int tile;                     // slots of a tile
+  int n_ctas, whole, atom;
+  int64_t max_atoms, pieces;    // pieces: partial results that may exist
+};
+KvAttnPlan kv_attn_plan(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int64_t max_len, int32_t window,
+                        bool invariant);
+cudaError_t launch_kv_attn(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p);
+
+// Whether csa_set_batch_invariant(1) is in force.
+bool batch_invariant();
 
 // Text returned by csa_last_error() for this thread.
 void set_last_error(const char* msg);

@@ -92,7 +92,8 @@ uint64_t csa_launch_count(void);
  * are non-NULL, the library records them on the call's stream immediately
  * before and after every launch of kernel `kernel_id`.  Pass NULLs to detach.
  * kernel_id: 0 = indexer scoring, 1 = top-k selection, 2 = attention,
- * 3 = split merge, 4 = compression, 5 = 4-bit quantization.
+ * 3 = split merge, 4 = compression, 5 = 4-bit quantization, 6 = top-k sampling,
+ * 7 = key-value append, 8 = key-value eviction.
  */
 csa_status_t csa_set_timing_events(int32_t kernel_id, void* ev_begin, void* ev_end);
 
@@ -517,6 +518,148 @@ csa_status_t hca_attn(const csa_bf16* q, const csa_cache_t* kv_comp, const csa_b
                       int32_t window, float sm_scale, const float* sink, csa_bf16* out,
                       float* lse, void* ws, size_t ws_bytes, csa_stream_t stream,
                       const csa_qrope_t* qrope);
+
+/* ---- per-head key-value caches ------------------------------------------- */
+/*
+ * A key-value cache whose every slot holds one key and one value per KV head:
+ * the raw-token cache of ordinary multi-head, grouped-query or multi-query
+ * attention (the eight-KV-head baseline of Ch.8 "A Cost Model for Long
+ * Context"), or, with k == v and one head, a shared-KV cache.
+ *   k, v        device, bf16 or fp16 (dtype), 16-byte aligned; element
+ *               (page, slot in page, head, coordinate c) is at
+ *               page*page_stride + slot*slot_stride + head*head_stride + c.
+ *               Strides are in elements, multiples of 8 and >= 0, so token-major
+ *               [pages, page_size, heads, d] and head-major [pages, heads,
+ *               page_size, d] caches, and keys and values interleaved in one
+ *               allocation, all fit
+ *   n_pages     physical pages that k and v hold (bounds for the checks)
+ *   page_table  device int32 [n_seq, max_pages]: slot s of sequence b is slot
+ *               s % page_size of page page_table[b*max_pages + s/page_size];
+ *               NULL: contiguous, sequence b is page b and max_pages is taken as 1
+ *   head_dim    a multiple of 8 in [8, 256]; page_size >= 1;
+ *               max_pages*page_size < 2^31
+ * A sequence with n tokens in the cache uses slots 0 .. n-1 (lens[b] = n).
+ * Calls that write a cache (append, evict) need every written slot to have a
+ * place of its own: strides that do not overlap and no page that two of the
+ * batch's sequences share there.
+ */
+typedef enum { CSA_KV_BF16 = 0, CSA_KV_FP16 = 1 } csa_kv_dtype_t;
+
+typedef struct {
+  void* k;
+  void* v;
+  int64_t n_pages;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  const int32_t* page_table;
+  int32_t max_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+} csa_kv_cache_t;
+
+/* Rows of [T, heads, d] in the cache's type: element (t, h, c) is at
+ * t*token_stride + h*head_stride + c (elements; multiples of 8), 16-byte
+ * aligned.  A slice of a fused projection's output fits. */
+typedef struct {
+  const void* data;
+  int64_t token_stride, head_stride;
+} csa_kv_rows_t;
+
+/*
+ * csa_kv_append -- write new tokens' keys and values behind each sequence's
+ * last slot.  Token t of sequence b (the i-th new one) goes to slot lens[b] + i
+ * of every head; lens_out[b] = lens[b] + the number of b's new tokens.
+ *   k_new, v_new  [n_tokens, n_kv_heads, d]
+ *   token_start   device int32 [B+1], ascending: sequence b's tokens are rows
+ *                 token_start[b] .. token_start[b+1]-1.  NULL: one token per
+ *                 sequence (n_tokens == B)
+ *   lens          device int32 [B]; lens_out [B] may be lens (in place)
+ *   weights       fp32 [B, n_kv_heads, slots], or NULL: set to 0 at the new slots
+ *   slot_pos      int32 [B, n_kv_heads, slots], or NULL: set to pos[b] + i there
+ *   pos           device int32 [B], required with slot_pos: position in the
+ *                 sequence of its first new token (eviction makes it differ
+ *                 from lens[b])
+ *   slots         row length of weights and slot_pos, at least every lens_out[b]
+ *   ws            at least 256 bytes (the device-check header)
+ * A token without room in the cache (or in `slots`), with a bad page id or of a
+ * sequence whose length is negative is dropped and recorded in the workspace;
+ * lens_out never exceeds the room.  k and v must not be the same memory.
+ */
+csa_status_t csa_kv_append(const csa_kv_rows_t* k_new, const csa_kv_rows_t* v_new,
+                           const csa_kv_cache_t* kv, const int32_t* token_start, int64_t n_tokens,
+                           int32_t B, const int32_t* lens, int32_t* lens_out, const int32_t* pos,
+                           float* weights, int32_t* slot_pos, int64_t slots, void* ws,
+                           size_t ws_bytes, csa_stream_t stream);
+
+/*
+ * csa_kv_attn_decode -- attention of one new token per sequence over its slots
+ * (the new token's own key and value appended before, csa_kv_append):
+ *   z[h,s] = sm_scale * q[b,h] . k[b,s,h/G],  G = H / n_kv_heads,
+ *   lse[b,h] = log(exp(sink[h]) + sum_s exp z[h,s]),
+ *   out[b,h] = sum_s exp(z[h,s] - lse[b,h]) v[b,s,h/G]
+ * over s in [max(0, lens[b] - window), lens[b]) (window = 0: all slots).  The
+ * slots of the whole batch are cut into equal shares for the GPU's SMs,
+ * whatever the lengths, and the shares' results joined (fixed 512-slot shares
+ * under csa_set_batch_invariant).  A sequence without slots gives zeros and the
+ * log of the sink's term (-inf without one).
+ *   q            [B, H, d] rows; H a multiple of n_kv_heads, G <= 128
+ *   lens         device int32 [B], 0 <= lens[b] <= max_len
+ *   max_len      at most max_pages*page_size; sizes the workspace.  A length
+ *                outside [0, max_len] is clamped and recorded in the workspace
+ *   sink         fp32 [H] or NULL;  out [B, H, d];  lse fp32 [B, H] or NULL
+ *   weights_out  fp32 [B, n_kv_heads, slots] or NULL: for s < lens[b],
+ *                weights_out[b,j,s] = weights[b,j,s] + sum over head j's group
+ *                of exp(z - lse) (weights NULL: 0 in its place).  weights may be
+ *                weights_out (accumulate in place); slots from lens[b] on are
+ *                left as they were.  Needs window == 0; slots >= max_len
+ * Slots on a bad page id are skipped and recorded.  Scores, softmax and output
+ * are accumulated in fp32; the probabilities are rounded to the cache's type for
+ * the product with the values.
+ */
+size_t csa_kv_attn_decode_workspace_size(int32_t B, int32_t H, const csa_kv_cache_t* kv,
+                                         int64_t max_len, int32_t with_weights);
+csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv,
+                                const int32_t* lens, int32_t B, int32_t H, int64_t max_len,
+                                int32_t window, float sm_scale, const float* sink, void* out,
+                                float* lse, const float* weights, float* weights_out,
+                                int64_t slots, void* ws, size_t ws_bytes, csa_stream_t stream);
+
+/*
+ * csa_kv_evict -- cut every sequence longer than `budget` slots down to it, head
+ * by head, by accumulated attention weight.  In each (sequence b, KV head):
+ *   - slots holding a recent token (slot_pos > pos[b] - recent) or one of the
+ *     first (slot_pos < keep_first) are held;
+ *   - the `budget` best slots stay: held ones first, then by weight, equal
+ *     weights (and held slots beyond the budget) by the lower slot; NaN counts
+ *     as above every number;
+ *   - the j-th slot below `budget` that did not stay takes the key, value,
+ *     weight and position of the j-th staying slot at or above it.  Other slots
+ *     keep theirs (so slots are not in token order afterwards: attention over
+ *     the cache does not depend on their order, a `window` over it would).
+ * lens_out[b] = min(lens[b], budget); sequences within the budget are unchanged.
+ * Keys and values above the budget are left as they were; pages wholly above it
+ * are free for other use.
+ *   pos                device int32 [B]: position of the newest token
+ *   recent >= 1, keep_first >= 0, recent + keep_first <= budget
+ *   weights, slot_pos  [B, n_kv_heads, slots], slots >= max_len; the *_out arrays
+ *                      may be the same memory (in place) or wholly apart.  They
+ *                      are written at 0 .. max_len-1, zeros from lens_out[b] on
+ *   lens               device int32 [B], lens[b] <= max_len; lens_out may be lens
+ *   src_out            int32 [B, n_kv_heads, budget] or NULL: the slot that each
+ *                      slot's row came from (itself if it stayed), -1 from
+ *                      lens_out[b] on; for arrays kept beside the cache
+ * A length outside [0, max_len] is clamped and recorded; a row on a bad page id is
+ * not copied and recorded.
+ */
+size_t csa_kv_evict_workspace_size(int32_t B, int32_t n_kv_heads, int32_t budget,
+                                   int64_t max_len);
+csa_status_t csa_kv_evict(const csa_kv_cache_t* kv, const int32_t* lens, int32_t* lens_out,
+                          const float* weights, float* weights_out, const int32_t* slot_pos,
+                          int32_t* slot_pos_out, int64_t slots, const int32_t* pos, int32_t B,
+                          int32_t budget, int32_t recent, int32_t keep_first, int64_t max_len,
+                          int32_t* src_out, void* ws, size_t ws_bytes, csa_stream_t stream);
 
 #ifdef __cplusplus
 }

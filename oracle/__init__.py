@@ -33,3 +33,4 @@ from .csa_oracle import (  # noqa: F401
 from . import cost_model  # noqa: F401
 from . import mxfp4  # noqa: F401
 from . import fp8_entry  # noqa: F401
+from .kv_oracle import kv_append, kv_attend, kv_evict, kv_place, kv_rows, kv_weigh  # noqa: F401
