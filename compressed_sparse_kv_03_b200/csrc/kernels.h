@@ -424,6 +424,7 @@ struct KvAttnArgs {
   float* lse2;                  // [B, H] log2 of the denominators (weights_out only)
   float* scores;                // [B, H, score_stride] scaled scores, base 2 (weights_out only)
   int64_t score_stride;
+  int32_t tiled;                // 1: rows come as TMA boxes (set by the launch)
   int32_t n_ctas;               // CTAs that share the tiles
   int32_t whole;                // 1: one CTA per unit, nothing to join
   int32_t atom;                 // tiles that stay together (batch-invariant: a slice)

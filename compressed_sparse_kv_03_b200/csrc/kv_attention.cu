@@ -13,8 +13,9 @@
 //   * 16 heads are the M side of mma.m16n8k16, 16 keys a step.  Up to 16 heads,
 //     the CTA's four warps take the tile's keys apart, each with a ring of its
 //     own (no block barrier in the loop); 32 and 64 heads put 2 and 4 warps
-//     side by side on the same keys.  Rows come by 16-byte cp.async into
-//     XOR-swizzled shared memory, page ids one step ahead of the copies.
+//     side by side on the same keys.  Rows come as TMA boxes of 16 rows (or,
+//     where 16 slots may lie on several pages, by cp.async), page ids one step
+//     ahead of them.
 //   * Softmax with a running maximum in base 2 and fp32; probabilities rounded
 //     to the cache's type for P V (as every 16-bit tensor-core product needs),
 //     their sum taken before that rounding.
@@ -22,6 +23,7 @@
 
 #include "kernels.h"
 #include "kv.cuh"
+#include "tc.cuh"
 
 namespace csa {
 
@@ -104,74 +106,113 @@ __device__ __forceinline__ int64_t share_of(const KvAttnArgs& a, int64_t atoms) 
   return (atoms + a.n_ctas - 1) / a.n_ctas;
 }
 
-// A position in the batch's list of tiles.
-struct Cursor {
-  int32_t b, hz, tile;
-  Span s;
-};
-
-// To the next sequence that has slots (a run's atoms lie on such sequences
-// only: there is one while atoms are left).
-template <int TILE>
-__device__ __forceinline__ bool next_sequence(const KvAttnArgs& a, Cursor& c) {
-  while (++c.b < a.B) {
-    c.s = span_of<TILE>(a, c.b, a.err);
-    if (c.s.tiles > 0) return true;
-  }
-  return false;
-}
-
 template <class T, int DP, int WH>
 struct Geometry {
   static constexpr int NG = 4 / WH;                 // key groups of a CTA
   static constexpr int TILE = kKeys * NG;
   static constexpr int GROUP = 32 * WH;             // threads of a key group
-  static constexpr int CH = DP / 8;                 // 16-byte pieces of a row
-  static constexpr int ROW = DP * 2;
-  static constexpr int STAGE = kKeys * ROW * 2;     // a group's keys and values
-  static constexpr int STAGES = DP == 64 ? 5 : DP == 128 ? 3 : DP == 192 ? 4 : 3;
-  static constexpr int RING = STAGES * STAGE * NG;
-  static constexpr int JOIN = NG > 1 ? NG / 2 * WH * 16 * DP * 4 : 0;
-  static constexpr int SMEM = RING + JOIN;
+  static constexpr int BOXES = DP / 64;             // 128-byte column blocks of a row
+  static constexpr int BOX = kKeys * 128;           // bytes of 16 rows of one
+  static constexpr int STAGE = 2 * BOXES * BOX;     // a group's keys, then values
+  static constexpr int STAGES = DP == 64 ? 6 : 3;
+  static constexpr int SMEM = STAGES * STAGE * NG + 1024;   // + alignment
   static constexpr int CTAS = DP <= 128 ? 2 : 1;    // resident per SM
+  // O of 16 heads fits a stage: joins go through the one that was just read
+  static_assert(STAGE == 16 * DP * 4, "a stage holds a warp's O");
 };
 
+// A position in this CTA's run of tiles.  A segment is the part of a unit that
+// the CTA takes in one go (in batch-invariant mode a slice): tiles [.., end).
+struct Cursor {
+  int32_t b, hz, tile, end;
+  int64_t left;   // atoms after this segment
+  Span s;
+};
+__device__ __forceinline__ void open_segment(const KvAttnArgs& a, Cursor& c) {
+  const int32_t rest = c.s.tiles - c.tile;
+  if (a.whole) {
+    c.end = c.s.tiles;
+    c.left = 0;
+  } else if (a.invariant) {
+    c.end = c.tile + (rest < a.atom ? rest : a.atom);
+    --c.left;
+  } else {
+    c.end = c.tile + (int32_t)(rest < c.left ? rest : c.left);
+    c.left -= c.end - c.tile;
+  }
+}
+// To the segment after the one that ends at c.tile; false: the run is over.
+template <int TILE>
+__device__ __forceinline__ bool next_segment(const KvAttnArgs& a, Cursor& c, int HZ) {
+  if (c.left <= 0) return false;
+  if (c.tile == c.s.tiles) {
+    c.tile = 0;
+    if (++c.hz == HZ) {
+      c.hz = 0;
+      do {
+        if (++c.b >= a.B) return false;
+        c.s = span_of<TILE>(a, c.b, a.err);
+      } while (c.s.tiles == 0);
+    }
+  }
+  open_segment(a, c);
+  return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Final scale and log-sum-exp (base 2) of a head from its maximum and sum.
+struct Norm {
+  float scale, lse2;
+};
+__device__ __forceinline__ Norm normalise(float m, float l, float z) {
+  const float M = fmaxf(m, z), R = M == -INFINITY ? 0.f : M;
+  const float f = exp2f(m - R);
+  const float L = l * f + exp2f(z - R);
+  return L == 0.f ? Norm{0.f, -INFINITY} : Norm{f / L, R + log2f(L)};
+}
+
 template <class T, int DP, int WH>
-__global__ void __launch_bounds__(kThreads, (Geometry<T, DP, WH>::CTAS)) kv_attn_kernel(KvAttnArgs a) {
+__global__ void __launch_bounds__(kThreads, (Geometry<T, DP, WH>::CTAS))
+kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+               const __grid_constant__ KvAttnArgs a) {
   using Geo = Geometry<T, DP, WH>;
-  constexpr int NG = Geo::NG, TILE = Geo::TILE, S = Geo::STAGES, CH = Geo::CH, ROW = Geo::ROW;
-  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int NG = Geo::NG, TILE = Geo::TILE, S = Geo::STAGES, BOX = Geo::BOX, BOXES = Geo::BOXES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // the swizzle's atoms are 1024 bytes
   __shared__ int64_t s_scan[8];
   __shared__ int64_t s_first[2];
   __shared__ float2 s_ml[4][16];
+  __shared__ __align__(8) uint64_t s_bar[NG][S];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kg = warp / WH, wh = warp % WH, gtid = tid % Geo::GROUP;
+  const int kg = warp / WH, wh = warp % WH;
   const int g = lane >> 2, t4 = lane & 3;
   const int G = a.H / a.n_kv_heads;
   const int blocks = (G + 16 * WH - 1) / (16 * WH);
   const int HZ = a.n_kv_heads * blocks;   // units of a sequence
   const uint32_t ring = smem_u32(smem) + kg * (S * Geo::STAGE);
-  float* const s_join = reinterpret_cast<float*>(smem + Geo::RING);
+  const uint32_t bars = smem_u32(&s_bar[kg][0]);
 
   // ---- this CTA's run of atoms ------------------------------------------------
   Cursor c;
-  int64_t atoms_left;
-  int64_t first_atom = 0;   // of the unit the run begins in, relative to that unit
   if (a.whole) {
     c.b = blockIdx.x / HZ;
     c.hz = blockIdx.x - c.b * HZ;
     c.s = span_of<TILE>(a, c.b, a.err);
     c.tile = 0;
-    atoms_left = 1;
   } else {
     int64_t all;
     atoms_before<TILE>(a, 0, &all, s_scan);
     all *= HZ;
     const int64_t share = share_of(a, all), begin = (int64_t)blockIdx.x * share;
-    atoms_left = all - begin < share ? all - begin : share;
-    if (atoms_left <= 0) return;
+    c.left = all - begin < share ? all - begin : share;
+    if (c.left <= 0) return;
     if (warp == 0) {   // the sequence that holds atom `begin`
       int64_t base = 0;
       for (int32_t b0 = 0; b0 < a.B; b0 += 32) {
@@ -200,81 +241,71 @@ __global__ void __launch_bounds__(kThreads, (Geometry<T, DP, WH>::CTAS)) kv_attn
     c.s = span_of<TILE>(a, c.b, a.err);
     const int64_t per_unit = (c.s.tiles + a.atom - 1) / a.atom;
     c.hz = (int32_t)(s_first[1] / per_unit);
-    first_atom = s_first[1] - c.hz * per_unit;
-    c.tile = (int32_t)(first_atom * a.atom);
+    c.tile = (int32_t)((s_first[1] - c.hz * per_unit) * a.atom);
   }
+  open_segment(a, c);
+  bool continued = c.tile > 0;   // the unit began before this run
+
+  const bool producer = wh == 0;
+  if (lane == 0 && producer) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) mbar_init(bars + 8 * i, a.tiled ? 1 : 32);
+    mbar_fence_init();
+  }
+  __syncthreads();
 
   // ---- copies -----------------------------------------------------------------
-  // The producer cursor runs S-1 steps ahead; the page ids of the step after
-  // that are already on their way.
+  // The first warp of a key group runs S-1 steps ahead of it, its page ids one
+  // step more.  Tiled (16 keys lie on one page: page_size a multiple of 16, or
+  // no page table): boxes of 16 rows by 128 bytes, one per lane; rows of the
+  // page behind the sequence come with them and are masked.  Otherwise 16 bytes
+  // a lane by cp.async, every row from its own page.
   Cursor p = c;
-  int64_t p_left = a.whole ? (c.s.tiles > 0 ? 1 : 0) : atoms_left;
-  const bool one_page = a.kv.table == nullptr || a.kv.page_size % kKeys == 0;
-  int32_t l_page = -1, l_row = 0;   // lookup of the producer cursor's step
+  bool p_live = c.s.tiles > 0;
+  int32_t l_page = -1, l_row = 0;
   auto lookup = [&]() {
-    const int32_t s0 = p.s.start + p.tile * TILE + kg * kKeys;
-    l_page = -1;
-    if (one_page) {
-      if (s0 < p.s.n) l_page = kv_page(a.kv, p.b, s0, &l_row, a.err);
-    } else {
-      const int32_t s = s0 + (lane & 15);
-      if (s >= p.s.lo && s < p.s.n) l_page = kv_page(a.kv, p.b, s, &l_row, a.err);
-    }
+    int32_t s = p.s.start + p.tile * TILE + kg * kKeys;
+    if (!a.tiled) s += lane & 15;
+    l_page = s < p.s.n && (a.tiled || s >= p.s.lo) ? kv_page(a.kv, p.b, s, &l_row, a.err) : -1;
   };
-  auto ends_atom = [&](const Cursor& x) {
-    return x.tile + 1 == x.s.tiles || (x.tile + 1) % a.atom == 0;
-  };
-  // Issue the copies of the producer cursor's step into ring slot `st`; returns
-  // the mask of its rows that exist.
+  // Start the copies of the producer cursor's step into ring slot `st`; returns
+  // the mask of its rows that the query sees.
   auto issue = [&](int st) -> uint32_t {
-    const int32_t s0 = p.s.start + p.tile * TILE + kg * kKeys;
+    const uint32_t bar = bars + 8 * st, dst = ring + st * Geo::STAGE;
+    const int h = p.hz / blocks;
     uint32_t rows = 0;
-    if (one_page) {
+    if (a.tiled) {
       if (l_page >= 0) {
-        const int32_t end = p.s.n - s0;
-        rows = end >= 16 ? 0xffffu : (1u << end) - 1u;
-        if (s0 < p.s.lo) rows &= p.s.lo - s0 >= 16 ? 0u : 0xffffu << (p.s.lo - s0);
+        const int32_t s0 = p.s.start + p.tile * TILE + kg * kKeys;
+        rows = p.s.n - s0 >= kKeys ? 0xffffu : (1u << (p.s.n - s0)) - 1u;
+        if (s0 < p.s.lo) rows &= 0xffffu << (p.s.lo - s0);   // at most 15: tiles start at lo rounded down
+      }
+      if (producer) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, l_page >= 0 ? Geo::STAGE : 0);
+        __syncwarp();
+        if (l_page >= 0 && lane < 2 * BOXES)
+          tc::tma_load_4d(dst + lane * BOX, lane < BOXES ? &map_k : &map_v, (lane % BOXES) * 64, h, l_row, l_page, bar);
       }
     } else {
       rows = __ballot_sync(0xffffffffu, l_page >= 0) & 0xffffu;
-    }
-    const int h = p.hz / blocks;
-    const char* const kb = a.kv.k + h * a.kv.k_head;
-    const char* const vb = a.kv.v + h * a.kv.v_head;
-    const int64_t page = l_page < 0 ? 0 : l_page;
-    int64_t ko = page * a.kv.k_page + l_row * a.kv.k_slot;
-    int64_t vo = page * a.kv.v_page + l_row * a.kv.v_slot;
-    const uint32_t dst = ring + st * Geo::STAGE;
-#pragma unroll
-    for (int i = 0; i < 16 * CH / Geo::GROUP; ++i) {
-      const int idx = i * Geo::GROUP + gtid, r = idx / CH, ch = idx % CH;
-      int64_t kro, vro;
-      if (one_page) {
-        kro = ko + r * a.kv.k_slot;
-        vro = vo + r * a.kv.v_slot;
-      } else {
-        kro = __shfl_sync(0xffffffffu, ko, r);
-        vro = __shfl_sync(0xffffffffu, vo, r);
-      }
-      const bool ok = ((rows >> r) & 1u) && ch * 8 < a.d;
-      const uint32_t at = dst + r * ROW + ((ch ^ (r & 7)) << 4);
-      cp_async_16(at, ok ? kb + kro + 16 * ch : a.kv.k, ok);
-      cp_async_16(at + kKeys * ROW, ok ? vb + vro + 16 * ch : a.kv.v, ok);
-    }
-    // step on
-    if (ends_atom(p)) {
-      if (a.whole ? p.tile + 1 == p.s.tiles : --p_left == 0) p_left = 0;
-    }
-    if (p_left > 0) {
-      if (++p.tile == p.s.tiles) {
-        p.tile = 0;
-        if (++p.hz == HZ) {
-          p.hz = 0;
-          if (!next_sequence<TILE>(a, p)) p_left = 0;
+      if (producer) {
+        const int64_t page = l_page < 0 ? 0 : l_page;
+        const int64_t ko = page * a.kv.k_page + l_row * a.kv.k_slot + h * a.kv.k_head;
+        const int64_t vo = page * a.kv.v_page + l_row * a.kv.v_slot + h * a.kv.v_head;
+#pragma unroll 4
+        for (int i = 0; i < 4 * BOXES; ++i) {   // 16 rows of 8 BOXES pieces
+          const int idx = i * 32 + lane, r = idx / (8 * BOXES), ch = idx % (8 * BOXES);
+          const int64_t kro = __shfl_sync(0xffffffffu, ko, r), vro = __shfl_sync(0xffffffffu, vo, r);
+          const bool ok = ((rows >> r) & 1u) && ch * 8 < a.d;
+          const uint32_t at = dst + (ch >> 3) * BOX + r * 128 + (((ch ^ r) & 7) << 4);
+          cp_async_16(at, ok ? a.kv.k + kro + 16 * ch : a.kv.k, ok);
+          cp_async_16(at + BOXES * BOX, ok ? a.kv.v + vro + 16 * ch : a.kv.v, ok);
         }
+        cp_async_mbar_arrive_noinc(bar);
       }
-      if (p_left > 0) lookup();
     }
+    if (++p.tile == p.end) p_live = next_segment<TILE>(a, p, HZ);
+    if (p_live) lookup();
     return rows;
   };
   auto group_sync = [&]() {
@@ -284,23 +315,20 @@ __global__ void __launch_bounds__(kThreads, (Geometry<T, DP, WH>::CTAS)) kv_attn
   };
 
   uint32_t rows_q[S - 1];   // masks of the steps in flight, oldest first
-  if (p_left > 0) lookup();
+  if (p_live) lookup();
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) {
-    rows_q[i] = p_left > 0 ? issue(i) : 0u;
-    cp_async_commit();
-  }
+  for (int i = 0; i < S - 1; ++i) rows_q[i] = p_live ? issue(i) : 0u;
 
-  // ---- units --------------------------------------------------------------------
+  // ---- segments -------------------------------------------------------------------
   int st = 0;   // ring slot of the current step
-  bool continued = first_atom > 0;   // the unit began before this run
+  uint32_t phase = 0;
+  bool dead = false;   // a wait ran out: no more waiting, the result is void
   const int kmat = lane >> 3, kr = lane & 7;
-  // ldmatrix rows: keys are non-transposed pairs (dims lo, hi of 8 keys), values
-  // transposed pairs (keys 0-7, 8-15 of 8 dims)
-  const uint32_t k_lane = (kr + (kmat >> 1) * 8) * ROW + (((kmat & 1) ^ kr) << 4);
-  const uint32_t v_lane = kKeys * ROW + (kr + (kmat & 1) * 8) * ROW + (((kmat >> 1) ^ kr) << 4);
-  bool more = a.whole || atoms_left > 0;
-  while (more) {
+  // ldmatrix rows: keys in non-transposed pairs (dims lo, hi of 8 keys), values in
+  // transposed ones (keys 0-7, 8-15 of 8 dims)
+  const uint32_t k_lane = (kr + (kmat >> 1) * 8) * 128 + (((kmat & 1) ^ kr) << 4);
+  const uint32_t v_lane = BOXES * BOX + (kr + (kmat & 1) * 8) * 128 + (((kmat >> 1) ^ kr) << 4);
+  for (bool more = true; more;) {
     const int kvh = c.hz / blocks, hb = c.hz - kvh * blocks;
     const int h_lo = hb * 16 * WH + wh * 16 + g;    // heads of the group that this lane's rows are
     const int h_hi = h_lo + 8;
@@ -323,61 +351,82 @@ __global__ void __launch_bounds__(kThreads, (Geometry<T, DP, WH>::CTAS)) kv_attn
     for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    // running maxima (of scaled scores, base 2) and this lane's part of the sums
     float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
     const int32_t first_tile = c.tile;
-    bool unit_done = c.s.tiles == 0;
-    if (unit_done) more = false;   // an empty sequence with a CTA to itself
-    while (!unit_done) {
-      cp_async_wait<S - 2>();
-      group_sync();   // the step's rows are in place, and everyone has left the slot that is filled next
+    float* sc = nullptr;
+    if (a.scores != nullptr)
+      sc = a.scores + (c.b * (int64_t)a.H + hq + h_lo) * a.score_stride + c.s.start + c.tile * TILE + kg * kKeys + 2 * t4;
+    for (; c.tile < c.end; ++c.tile) {
+      if (!dead && !mbar_wait(bars + 8 * st, phase)) {
+        dead = true;
+        report(a.err, kErrTimeout, c.b, c.tile);
+      }
+      group_sync();   // everyone has left the slot that is filled next
       const uint32_t rows = rows_q[0];
 #pragma unroll
       for (int i = 0; i + 1 < S - 1; ++i) rows_q[i] = rows_q[i + 1];
-      {
-        const int nst = st == 0 ? S - 1 : st - 1;
-        rows_q[S - 2] = p_left > 0 ? issue(nst) : 0u;
-        cp_async_commit();
-      }
+      rows_q[S - 2] = p_live ? issue(st == 0 ? S - 1 : st - 1) : 0u;
       const uint32_t base = ring + st * Geo::STAGE;
-      st = st + 1 == S ? 0 : st + 1;
-
-      float s[2][4] = {};
-#pragma unroll
-      for (int ks = 0; ks < DP / 16; ++ks) {
-        uint32_t kb[4];
-        ldmatrix_x4(kb, base + (ks >> 2) * 128 + (k_lane ^ ((ks & 3) * 32)));
-        mma16816<T>(s[0], q[ks], kb[0], kb[1]);
-        mma16816<T>(s[1], q[ks], kb[2], kb[3]);
+      if (++st == S) {
+        st = 0;
+        phase ^= 1u;
       }
+
+      float sa[2][4] = {}, sb[2][4] = {};   // even and odd k-steps: shorter chains
+#pragma unroll
+      for (int ks = 0; ks < DP / 16; ks += 2) {
+        uint32_t k0[4], k1[4];
+        ldmatrix_x4(k0, base + (ks >> 2) * BOX + (k_lane ^ ((ks & 3) * 32)));
+        ldmatrix_x4(k1, base + (ks >> 2) * BOX + (k_lane ^ ((ks & 3) * 32 + 32)));
+        mma16816<T>(sa[0], q[ks], k0[0], k0[1]);
+        mma16816<T>(sa[1], q[ks], k0[2], k0[3]);
+        mma16816<T>(sb[0], q[ks + 1], k1[0], k1[1]);
+        mma16816<T>(sb[1], q[ks + 1], k1[2], k1[3]);
+      }
+      float s[2][4];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int key = nt * 8 + 2 * t4 + (j & 1);
-          s[nt][j] = (rows >> key) & 1u ? s[nt][j] * a.scale : -INFINITY;
+        for (int j = 0; j < 4; ++j) s[nt][j] = (sa[nt][j] + sb[nt][j]) * a.scale;
+      if (rows != 0xffffu) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((rows >> (nt * 8 + 2 * t4 + (j & 1))) & 1u)) s[nt][j] = -INFINITY;
+        // 0 times what lies in an unseen value row may be NaN: clear those rows
+        // (every warp of the group all of them, so that none waits for another)
+        for (int i = lane; i < kKeys * BOXES * 8; i += 32) {
+          const int r = (i >> 3) & (kKeys - 1);
+          if (!((rows >> r) & 1u))
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(base + BOXES * BOX + i * 16), "r"(0u) : "memory");
         }
+        fence_async_smem_cta();
+        __syncwarp();
+      }
       if (a.scores != nullptr) {
         const int32_t s0 = c.s.start + c.tile * TILE + kg * kKeys + 2 * t4;
-        float* const w = a.scores + (c.b * (int64_t)a.H + hq) * a.score_stride + s0;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           if (s0 + nt * 8 < c.s.n) {   // rows hold an even number of slots
-            if (h_lo < G) *reinterpret_cast<float2*>(w + h_lo * a.score_stride + nt * 8) = make_float2(s[nt][0], s[nt][1]);
-            if (h_hi < G) *reinterpret_cast<float2*>(w + h_hi * a.score_stride + nt * 8) = make_float2(s[nt][2], s[nt][3]);
+            if (h_lo < G) *reinterpret_cast<float2*>(sc + nt * 8) = make_float2(s[nt][0], s[nt][1]);
+            if (h_hi < G) *reinterpret_cast<float2*>(sc + 8 * a.score_stride + nt * 8) = make_float2(s[nt][2], s[nt][3]);
           }
         }
+        sc += TILE;
       }
       float x_lo = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
       float x_hi = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+      if (__any_sync(0xffffffffu, x_lo > m_lo || x_hi > m_hi)) {   // some row's maximum grows
 #pragma unroll
-      for (int off = 1; off <= 2; off <<= 1) {
-        x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, off));
-        x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, off));
-      }
-      if (__any_sync(0xffffffffu, x_lo > m_lo || x_hi > m_hi)) {
+        for (int off = 1; off <= 2; off <<= 1) {
+          x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, off));
+          x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, off));
+        }
         const float n_lo = fmaxf(m_lo, x_lo), n_hi = fmaxf(m_hi, x_hi);
-        const float f_lo = n_lo == -INFINITY ? 1.f : exp2f(m_lo - n_lo);
-        const float f_hi = n_hi == -INFINITY ? 1.f : exp2f(m_hi - n_hi);
+        const float f_lo = n_lo == -INFINITY ? 1.f : ex2(m_lo - n_lo);
+        const float f_hi = n_hi == -INFINITY ? 1.f : ex2(m_hi - n_hi);
         m_lo = n_lo;
         m_hi = n_hi;
         l_lo *= f_lo;
@@ -394,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, (Geometry<T, DP, WH>::CTAS)) kv_attn
       uint32_t pa[4];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        const float p0 = exp2f(s[nt][0] - r_lo), p1 = exp2f(s[nt][1] - r_lo);
-        const float p2 = exp2f(s[nt][2] - r_hi), p3 = exp2f(s[nt][3] - r_hi);
+        const float p0 = ex2(s[nt][0] - r_lo), p1 = ex2(s[nt][1] - r_lo);
+        const float p2 = ex2(s[nt][2] - r_hi), p3 = ex2(s[nt][3] - r_hi);
         l_lo += p0 + p1;
         l_hi += p2 + p3;
         pa[2 * nt] = pack2<T>(p0, p1);
@@ -404,146 +453,165 @@ __global__ void __launch_bounds__(kThreads, (Geometry<T, DP, WH>::CTAS)) kv_attn
 #pragma unroll
       for (int j = 0; j < DP / 16; ++j) {
         uint32_t vb[4];
-        ldmatrix_x4_trans(vb, base + (j >> 2) * 128 + (v_lane ^ ((j & 3) * 32)));
+        ldmatrix_x4_trans(vb, base + (j >> 2) * BOX + (v_lane ^ ((j & 3) * 32)));
         mma16816<T>(o[2 * j], pa, vb[0], vb[1]);
         mma16816<T>(o[2 * j + 1], pa, vb[2], vb[3]);
       }
-
-      // next tile
-      const bool last = c.tile + 1 == c.s.tiles;
-      const bool atom_end = last || (c.tile + 1) % a.atom == 0;
-      if (a.whole) {
-        unit_done = last;
-        more = !last;
-      } else {
-        if (atom_end) --atoms_left;
-        unit_done = last || atoms_left == 0 || (a.invariant && atom_end);
-        more = atoms_left > 0;
-      }
-      ++c.tile;
     }
 
     // ---- join the key groups, store --------------------------------------------
+    // Everyone has read slot st - 1 to the end; the next step fills it.
 #pragma unroll
     for (int off = 1; off <= 2; off <<= 1) {
       l_lo += __shfl_xor_sync(0xffffffffu, l_lo, off);
       l_hi += __shfl_xor_sync(0xffffffffu, l_hi, off);
     }
-    if constexpr (NG > 1) {
+    const bool whole_unit = first_tile == 0 && c.tile == c.s.tiles;   // no other piece exists
+    const int64_t bh = (int64_t)c.b * a.H + hq;
+    const int64_t piece = a.invariant ? ((int64_t)c.b * HZ + c.hz) * a.max_atoms + first_tile / a.atom
+                                      : 2 * (int64_t)blockIdx.x + (continued ? 0 : 1);
+    // Stores 4 (or 2) neighbouring columns of a row of heads.
+    auto store_ml = [&](int row, float m, float l) {   // row: of the head block
+      const int h = hb * 16 * WH + row;
+      if (!whole_unit) {
+        *reinterpret_cast<float2*>(a.part_ml + (piece * (16 * WH) + row) * 2) = make_float2(m, l);
+      } else if (h < G) {
+        const Norm nm = normalise(m, l, a.sink ? a.sink[hq + h] * kLog2e : -INFINITY);
+        if (a.lse) a.lse[bh + h] = nm.lse2 * (1.f / kLog2e);
+        if (a.lse2) a.lse2[bh + h] = nm.lse2;
+      }
+    };
+    if constexpr (NG == 4) {
+      // every warp puts its O down and sums a quarter of the columns of all four
+      const int prev = st == 0 ? S - 1 : st - 1;
+      float* const mine = reinterpret_cast<float*>(smem + (kg * S + prev) * Geo::STAGE);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < DP / 8; ++i) {
+        // 8-float blocks permuted by row, off the bank conflicts
+        const int at = ((i ^ (g & 3)) * 8) + 2 * t4;
+        *reinterpret_cast<float2*>(mine + g * DP + at) = make_float2(o[i][0], o[i][1]);
+        *reinterpret_cast<float2*>(mine + (g + 8) * DP + at) = make_float2(o[i][2], o[i][3]);
+      }
       if (t4 == 0) {
         s_ml[warp][g] = make_float2(m_lo, l_lo);
         s_ml[warp][g + 8] = make_float2(m_hi, l_hi);
       }
       __syncthreads();
-      float M_lo = -INFINITY, M_hi = -INFINITY;
+      constexpr int F4 = DP / 16;   // float4 per row of a quarter
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        M_lo = fmaxf(M_lo, s_ml[i * WH + wh][g].x);
-        M_hi = fmaxf(M_hi, s_ml[i * WH + wh][g + 8].x);
+      for (int i = 0; i < 16 * F4 / 32; ++i) {
+        const int idx = i * 32 + lane, row = idx / F4, col = warp * (DP / 4) + (idx % F4) * 4;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = fmaxf(m, s_ml[w][row].x);
+        const float R = m == -INFINITY ? 0.f : m;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 ml = s_ml[w][row];
+          const float f = ex2(ml.x - R);
+          l = fmaf(ml.y, f, l);
+          const float4 x = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(smem + (w * S + prev) * Geo::STAGE) + row * DP + (col ^ ((row & 3) * 8)));
+          acc.x = fmaf(x.x, f, acc.x);
+          acc.y = fmaf(x.y, f, acc.y);
+          acc.z = fmaf(x.z, f, acc.z);
+          acc.w = fmaf(x.w, f, acc.w);
+        }
+        const int h = hb * 16 + row;
+        if (whole_unit) {
+          if (h < G && col < a.d) {
+            const float k = normalise(m, l, a.sink ? a.sink[hq + h] * kLog2e : -INFINITY).scale;
+            uint2 pk;
+            pk.x = pack2<T>(acc.x * k, acc.y * k);
+            pk.y = pack2<T>(acc.z * k, acc.w * k);
+            *reinterpret_cast<uint2*>(a.out + ((bh + h) * a.d + col) * 2) = pk;
+          }
+        } else {
+          *reinterpret_cast<float4*>(a.part_acc + (piece * 16 + row) * DP + col) = acc;
+        }
+        if (col == 0) store_ml(row, m, l);
       }
-      const float R_lo = M_lo == -INFINITY ? 0.f : M_lo, R_hi = M_hi == -INFINITY ? 0.f : M_hi;
-      l_lo = l_hi = 0.f;
+      fence_async_smem_cta();
+      __syncthreads();   // the slots may be filled again
+    } else {
+      if constexpr (NG == 2) {   // group 1 hands its O to group 0 through both groups' slots
+        const int prev = st == 0 ? S - 1 : st - 1;
+        float2* const buf = reinterpret_cast<float2*>(smem + (wh * S + prev) * Geo::STAGE) + lane;
+        if (t4 == 0) {
+          s_ml[warp][g] = make_float2(m_lo, l_lo);
+          s_ml[warp][g + 8] = make_float2(m_hi, l_hi);
+        }
+        __syncthreads();   // and both groups have left their slots
+        const float2 x_lo = s_ml[(1 - kg) * WH + wh][g], x_hi = s_ml[(1 - kg) * WH + wh][g + 8];
+        const float M_lo = fmaxf(m_lo, x_lo.x), M_hi = fmaxf(m_hi, x_hi.x);
+        const float R_lo = M_lo == -INFINITY ? 0.f : M_lo, R_hi = M_hi == -INFINITY ? 0.f : M_hi;
+        const float f_lo = ex2(m_lo - R_lo), f_hi = ex2(m_hi - R_hi);
+        l_lo = l_lo * f_lo + x_lo.y * ex2(x_lo.x - R_lo);
+        l_hi = l_hi * f_hi + x_hi.y * ex2(x_hi.x - R_hi);
+        m_lo = M_lo;
+        m_hi = M_hi;
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const float2 x = s_ml[i * WH + wh][g], y = s_ml[i * WH + wh][g + 8];
-        l_lo += x.y * exp2f(x.x - R_lo);
-        l_hi += y.y * exp2f(y.x - R_hi);
-      }
-      const float f_lo = exp2f(m_lo - R_lo), f_hi = exp2f(m_hi - R_hi);
-      m_lo = M_lo;
-      m_hi = M_hi;
-#pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
-        o[i][0] *= f_lo;
-        o[i][1] *= f_lo;
-        o[i][2] *= f_hi;
-        o[i][3] *= f_hi;
-      }
-      // groups half, half+1, .. hand theirs down, log2(NG) times
-#pragma unroll
-      for (int half = NG / 2; half >= 1; half >>= 1) {
-        float4* const buf = reinterpret_cast<float4*>(s_join) + (((kg % half) * WH + wh) * (DP / 8)) * 32 + lane;
-        if (kg >= half && kg < 2 * half) {
-#pragma unroll
-          for (int i = 0; i < DP / 8; ++i) buf[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        for (int i = 0; i < DP / 8; ++i) {
+          o[i][0] *= f_lo;
+          o[i][1] *= f_lo;
+          o[i][2] *= f_hi;
+          o[i][3] *= f_hi;
+          if (kg == 1) {
+            buf[(2 * i) * 32] = make_float2(o[i][0], o[i][1]);
+            buf[(2 * i + 1) * 32] = make_float2(o[i][2], o[i][3]);
+          }
         }
         __syncthreads();
-        if (kg < half) {
+        if (kg == 0) {
 #pragma unroll
           for (int i = 0; i < DP / 8; ++i) {
-            const float4 x = buf[i * 32];
+            const float2 x = buf[(2 * i) * 32], y = buf[(2 * i + 1) * 32];
             o[i][0] += x.x;
             o[i][1] += x.y;
-            o[i][2] += x.z;
-            o[i][3] += x.w;
+            o[i][2] += y.x;
+            o[i][3] += y.y;
           }
         }
-        if (half > 1) __syncthreads();
+        fence_async_smem_cta();
+        __syncthreads();
       }
-    }
-    const bool whole_unit = first_tile == 0 && c.tile == c.s.tiles;   // no other piece exists
-    if (kg == 0) {
-      const int64_t bh = (int64_t)c.b * a.H + hq;
-      if (whole_unit) {
-        const float z_lo = a.sink && h_lo < G ? a.sink[hq + h_lo] * kLog2e : -INFINITY;
-        const float z_hi = a.sink && h_hi < G ? a.sink[hq + h_hi] * kLog2e : -INFINITY;
-        const float M_lo = fmaxf(m_lo, z_lo), M_hi = fmaxf(m_hi, z_hi);
-        const float R_lo = M_lo == -INFINITY ? 0.f : M_lo, R_hi = M_hi == -INFINITY ? 0.f : M_hi;
-        const float f_lo = exp2f(m_lo - R_lo), f_hi = exp2f(m_hi - R_hi);
-        const float L_lo = l_lo * f_lo + exp2f(z_lo - R_lo), L_hi = l_hi * f_hi + exp2f(z_hi - R_hi);
-        const float i_lo = L_lo == 0.f ? 0.f : f_lo / L_lo, i_hi = L_hi == 0.f ? 0.f : f_hi / L_hi;
-        if (t4 == 0) {
-          const float e_lo = L_lo == 0.f ? -INFINITY : R_lo + log2f(L_lo);
-          const float e_hi = L_hi == 0.f ? -INFINITY : R_hi + log2f(L_hi);
-          if (a.lse) {
-            if (h_lo < G) a.lse[bh + h_lo] = e_lo * (1.f / kLog2e);
-            if (h_hi < G) a.lse[bh + h_hi] = e_hi * (1.f / kLog2e);
-          }
-          if (a.lse2) {
-            if (h_lo < G) a.lse2[bh + h_lo] = e_lo;
-            if (h_hi < G) a.lse2[bh + h_hi] = e_hi;
-          }
-        }
-        char* const out_lo = a.out + (bh + h_lo) * a.d * 2;
-        char* const out_hi = out_lo + 8 * a.d * 2;
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          const int d0 = i * 8 + 2 * t4;
-          if (d0 < a.d) {
-            if (h_lo < G) *reinterpret_cast<uint32_t*>(out_lo + 2 * d0) = pack2<T>(o[i][0] * i_lo, o[i][1] * i_lo);
-            if (h_hi < G) *reinterpret_cast<uint32_t*>(out_hi + 2 * d0) = pack2<T>(o[i][2] * i_hi, o[i][3] * i_hi);
-          }
-        }
-      } else {
-        const int64_t unit = (int64_t)c.b * HZ + c.hz;
-        const int64_t piece = a.invariant ? unit * a.max_atoms + first_tile / a.atom
-                                          : 2 * (int64_t)blockIdx.x + (continued ? 0 : 1);
+      if (kg == 0) {
         const int row = wh * 16 + g;
-        float* const acc = a.part_acc + (piece * (16 * WH) + row) * DP;
-        float* const ml = a.part_ml + (piece * (16 * WH) + row) * 2;
         if (t4 == 0) {
-          *reinterpret_cast<float2*>(ml) = make_float2(m_lo, l_lo);
-          *reinterpret_cast<float2*>(ml + 16) = make_float2(m_hi, l_hi);
+          store_ml(row, m_lo, l_lo);
+          store_ml(row + 8, m_hi, l_hi);
         }
+        if (whole_unit) {
+          const float k_lo = h_lo < G ? normalise(m_lo, l_lo, a.sink ? a.sink[hq + h_lo] * kLog2e : -INFINITY).scale : 0.f;
+          const float k_hi = h_hi < G ? normalise(m_hi, l_hi, a.sink ? a.sink[hq + h_hi] * kLog2e : -INFINITY).scale : 0.f;
+          char* const out_lo = a.out + (bh + h_lo) * a.d * 2;
+          char* const out_hi = out_lo + 8 * a.d * 2;
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          *reinterpret_cast<float2*>(acc + i * 8 + 2 * t4) = make_float2(o[i][0], o[i][1]);
-          *reinterpret_cast<float2*>(acc + 8 * DP + i * 8 + 2 * t4) = make_float2(o[i][2], o[i][3]);
+          for (int i = 0; i < DP / 8; ++i) {
+            const int d0 = i * 8 + 2 * t4;
+            if (d0 < a.d) {
+              if (h_lo < G) *reinterpret_cast<uint32_t*>(out_lo + 2 * d0) = pack2<T>(o[i][0] * k_lo, o[i][1] * k_lo);
+              if (h_hi < G) *reinterpret_cast<uint32_t*>(out_hi + 2 * d0) = pack2<T>(o[i][2] * k_hi, o[i][3] * k_hi);
+            }
+          }
+        } else {
+          float* const acc = a.part_acc + (piece * (16 * WH) + row) * DP;
+#pragma unroll
+          for (int i = 0; i < DP / 8; ++i) {
+            *reinterpret_cast<float2*>(acc + i * 8 + 2 * t4) = make_float2(o[i][0], o[i][1]);
+            *reinterpret_cast<float2*>(acc + 8 * DP + i * 8 + 2 * t4) = make_float2(o[i][2], o[i][3]);
+          }
         }
       }
     }
     continued = false;
-    if (more) {
-      if (c.tile == c.s.tiles) {
-        c.tile = 0;
-        if (++c.hz == HZ) {
-          c.hz = 0;
-          if (!next_sequence<TILE>(a, c)) more = false;
-        }
-      }
-    }
+    more = next_segment<TILE>(a, c, HZ);
   }
-  cp_async_wait<0>();
+  if (dead) {   // copies may still be under way: wait for them, within a limit
+    for (int i = 0; i < S; ++i) mbar_wait(bars + 8 * i, phase, 200000000ll);
+  }
 }
 
 // ---- joining --------------------------------------------------------------------
@@ -685,13 +753,34 @@ __global__ void __launch_bounds__(kThreads) kv_finish_kernel(KvAttnArgs a, int j
   }
 }
 
+// Tensor map of a cache's keys or values, [page][slot][head][coordinate], if 16
+// consecutive slots from a multiple of 16 on lie on one page and no dimension is
+// broadcast (a stride of 0).
+bool tile_map(const char* data, int64_t page_st, int64_t slot_st, int64_t head_st, const KvAttnArgs& a, CUtensorMap* map) {
+  const KvRef& kv = a.kv;
+  if (kv.table != nullptr && kv.page_size % kKeys != 0) return false;
+  const uint64_t dims[4] = {(uint64_t)a.d, (uint64_t)a.n_kv_heads, (uint64_t)kv.page_size, (uint64_t)kv.n_pages};
+  int64_t st[3] = {head_st, slot_st, page_st};
+  for (int i = 0; i < 3; ++i) {
+    if (dims[i + 1] == 1) st[i] = (int64_t)a.d * 2 + (-(int64_t)a.d * 2 & 15);   // never stepped over
+    if (st[i] <= 0 || st[i] >= (int64_t(1) << 40)) return false;
+  }
+  const uint64_t strides[3] = {(uint64_t)st[0], (uint64_t)st[1], (uint64_t)st[2]};
+  return make_tmap_16bit_4d(map, data, dims, strides, 64, kKeys);
+}
+
 template <class T, int DP, int WH>
-cudaError_t launch_typed(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p) {
+cudaError_t launch_typed(const Launch& L, const KvAttnArgs& args, const KvAttnPlan& p) {
   using Geo = Geometry<T, DP, WH>;
   cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<T, DP, WH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::SMEM);
   if (e != cudaSuccess) return e;
+  KvAttnArgs a = args;
+  CUtensorMap map_k = {}, map_v = {};
+  a.tiled = tile_map(a.kv.k, a.kv.k_page, a.kv.k_slot, a.kv.k_head, a, &map_k) &&
+            tile_map(a.kv.v, a.kv.v_page, a.kv.v_slot, a.kv.v_head, a, &map_v);
   L.begin(kKernelAttention);
-  e = launch_kernel(kv_attn_kernel<T, DP, WH>, dim3((unsigned)p.n_ctas), dim3(kThreads), Geo::SMEM, L.stream, true, a);
+  e = launch_kernel(kv_attn_kernel<T, DP, WH>, dim3((unsigned)p.n_ctas), dim3(kThreads), Geo::SMEM, L.stream, true, map_k,
+                    map_v, a);
   if (e != cudaSuccess) return e;
   e = L.end(kKernelAttention);
   if (e != cudaSuccess || (p.whole && a.weights_out == nullptr)) return e;

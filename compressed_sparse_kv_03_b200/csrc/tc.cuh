@@ -161,6 +161,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x,
+                                            int32_t y, int32_t z, int32_t w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -170,6 +178,11 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
 // Host: encode a 2-D bf16 tensor map over `rows` rows of `cols` elements
 // (row pitch `pitch_elems`), box = [box_cols, box_rows], 128-byte swizzle,
 // out-of-bounds rows read as zero.  Returns false on failure.
+// 4-D map of 16-bit elements, boxes of box_cols x 1 x box_dim2 x 1 in the
+// 128-byte swizzle, zeros outside (strides of dimensions 1 to 3, in bytes);
+// false when the driver does not take the geometry.
+bool make_tmap_16bit_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                        const uint64_t (&strides_bytes)[3], uint32_t box_cols, uint32_t box_dim2);
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                        uint64_t pitch_elems, uint32_t box_cols, uint32_t box_rows);
 

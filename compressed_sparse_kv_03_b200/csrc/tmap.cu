@@ -37,4 +37,18 @@ bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64
   return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_16bit_4d(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                        const uint64_t (&strides_bytes)[3], uint32_t box_cols, uint32_t box_dim2) {
+  std::call_once(g_encode_once, resolve_encode);
+  if (g_encode == nullptr) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t s[3] = {strides_bytes[0], strides_bytes[1], strides_bytes[2]};
+  const cuuint32_t box[4] = {box_cols, 1, box_dim2, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), d, s,
+                              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace csa
