@@ -434,7 +434,8 @@ struct KvAttnArgs {
 };
 // Geometry of a call, shared by the workspace size and the launch.
 struct KvAttnPlan {
-  int wh;                       // 16-head warps side by side in a CTA
+  int nb, wh;                   // blocks of 8 heads per warp, warps side by side in a CTA
+  int heads;                    // of a unit: 8 nb wh
   int blocks;                   // head blocks of a group
   int dp;                       // padded head dim
   int tile;                     // slots of a tile

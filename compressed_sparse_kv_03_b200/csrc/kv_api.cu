@@ -150,7 +150,7 @@ AttnLayout attn_layout(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int6
                        bool weights) {
   AttnLayout l;
   l.plan = kv_attn_plan(B, H, n_kv_heads, d, max_len, window, batch_invariant());
-  const size_t rows = (size_t)l.plan.pieces * 16 * l.plan.wh;
+  const size_t rows = (size_t)l.plan.pieces * l.plan.heads;
   l.ml_off = kWsHeader;
   l.acc_off = l.ml_off + align256(rows * 2 * sizeof(float));
   l.lse_off = l.acc_off + align256(rows * l.plan.dp * sizeof(float));

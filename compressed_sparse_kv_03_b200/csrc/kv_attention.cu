@@ -10,8 +10,9 @@
 //     through its run without draining its copies between units; a unit that
 //     spans several CTAs leaves partial (O, max, sum) pieces that a second
 //     kernel joins in CTA order.
-//   * 16 heads are the M side of mma.m16n8k16, 16 keys a step.  Up to 16 heads,
-//     the CTA's four warps take the tile's keys apart, each with a ring of its
+//   * Keys are the M side of mma.m16n8k16, 16 a step, heads the N side, 8 or 16
+//     a warp (mma.sync's rate on this chip is an eighth of tcgen05's, so the
+//     columns matter).  Up to 16 heads, the CTA's four warps take the tile's keys apart, each with a ring of its
 //     own (no block barrier in the loop); 32 and 64 heads put 2 and 4 warps
 //     side by side on the same keys.  Rows come as TMA boxes of 16 rows (or,
 //     where 16 slots may lie on several pages, by cp.async), page ids one step
@@ -76,29 +77,31 @@ __device__ __forceinline__ Span span_of(const KvAttnArgs& a, int32_t b, WsHeader
   return s;
 }
 
-// Atoms before sequence `b` and in the whole batch, per unit of a sequence;
-// every thread of the block gets both (128 threads).
 template <int TILE>
-__device__ int64_t atoms_before(const KvAttnArgs& a, int32_t b, int64_t* all, int64_t* scratch) {
-  int64_t before = 0, total = 0;
-  for (int32_t i = threadIdx.x; i < a.B; i += kThreads) {
-    const int64_t t = (span_of<TILE>(a, i, nullptr).tiles + a.atom - 1) / a.atom;
-    total += t;
-    if (i < b) before += t;
-  }
+__device__ __forceinline__ int64_t atoms_of(const KvAttnArgs& a, int32_t b) {   // of a unit of sequence b
+  return (span_of<TILE>(a, b, nullptr).tiles + a.atom - 1) / a.atom;
+}
+
+// Sum over the block's 128 threads, and of the threads before this one.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* before, int64_t* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t up = x;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += v;
   }
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    scratch[threadIdx.x >> 5] = before;
-    scratch[4 + (threadIdx.x >> 5)] = total;
-  }
+  if (lane == 31) scratch[warp] = up;
   __syncthreads();
-  *all = scratch[4] + scratch[5] + scratch[6] + scratch[7];
-  return scratch[0] + scratch[1] + scratch[2] + scratch[3];
+  int64_t base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) base += scratch[w];
+    all += scratch[w];
+  }
+  *before = base + up - x;
+  return all;
 }
 
 // Atoms per CTA: equal shares.
@@ -106,17 +109,23 @@ __device__ __forceinline__ int64_t share_of(const KvAttnArgs& a, int64_t atoms) 
   return (atoms + a.n_ctas - 1) / a.n_ctas;
 }
 
-template <class T, int DP, int WH>
+// Resident CTAs per SM: registers (at most 128 a thread with 8 heads a warp, 255
+// with 16) and the ring allow that many.
+constexpr int ctas_per_sm(int dp, int nb) { return dp == 64 ? 4 / nb : dp == 128 ? 2 : 1; }
+
+// NB blocks of 8 heads per warp, WH warps side by side.
+template <class T, int DP, int NB, int WH>
 struct Geometry {
   static constexpr int NG = 4 / WH;                 // key groups of a CTA
   static constexpr int TILE = kKeys * NG;
   static constexpr int GROUP = 32 * WH;             // threads of a key group
+  static constexpr int HEADS = 8 * NB * WH;         // of a unit
   static constexpr int BOXES = DP / 64;             // 128-byte column blocks of a row
   static constexpr int BOX = kKeys * 128;           // bytes of 16 rows of one
   static constexpr int STAGE = 2 * BOXES * BOX;     // a group's keys, then values
-  static constexpr int STAGES = DP == 64 ? 6 : 3;
+  static constexpr int CTAS = ctas_per_sm(DP, NB);
+  static constexpr int STAGES = DP == 64 && CTAS == 2 ? 6 : 3;
   static constexpr int SMEM = STAGES * STAGE * NG + 1024;   // + alignment
-  static constexpr int CTAS = DP <= 128 ? 2 : 1;    // resident per SM
   // O of 16 heads fits a stage: joins go through the one that was just read
   static_assert(STAGE == 16 * DP * 4, "a stage holds a warp's O");
 };
@@ -159,6 +168,13 @@ __device__ __forceinline__ bool next_segment(const KvAttnArgs& a, Cursor& c, int
   return true;
 }
 
+// Transposes an 8 x 8 matrix of 16-bit values held as (row lane/4, columns 2 (lane%4), +1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -176,17 +192,17 @@ __device__ __forceinline__ Norm normalise(float m, float l, float z) {
   return L == 0.f ? Norm{0.f, -INFINITY} : Norm{f / L, R + log2f(L)};
 }
 
-template <class T, int DP, int WH>
-__global__ void __launch_bounds__(kThreads, (Geometry<T, DP, WH>::CTAS))
+template <class T, int DP, int NB, int WH>
+__global__ void __launch_bounds__(kThreads, (Geometry<T, DP, NB, WH>::CTAS))
 kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                const __grid_constant__ KvAttnArgs a) {
-  using Geo = Geometry<T, DP, WH>;
-  constexpr int NG = Geo::NG, TILE = Geo::TILE, S = Geo::STAGES, BOX = Geo::BOX, BOXES = Geo::BOXES;
+  using Geo = Geometry<T, DP, NB, WH>;
+  constexpr int NG = Geo::NG, TILE = Geo::TILE, S = Geo::STAGES, BOX = Geo::BOX, BOXES = Geo::BOXES, HEADS = Geo::HEADS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // the swizzle's atoms are 1024 bytes
-  __shared__ int64_t s_scan[8];
+  __shared__ int64_t s_scan[4];
   __shared__ int64_t s_first[2];
-  __shared__ float2 s_ml[4][16];
+  __shared__ float2 s_ml[4][HEADS];
   __shared__ __align__(8) uint64_t s_bar[NG][S];
   pdl_wait();
   pdl_trigger();
@@ -194,7 +210,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   const int kg = warp / WH, wh = warp % WH;
   const int g = lane >> 2, t4 = lane & 3;
   const int G = a.H / a.n_kv_heads;
-  const int blocks = (G + 16 * WH - 1) / (16 * WH);
+  const int blocks = (G + HEADS - 1) / HEADS;
   const int HZ = a.n_kv_heads * blocks;   // units of a sequence
   const uint32_t ring = smem_u32(smem) + kg * (S * Geo::STAGE);
   const uint32_t bars = smem_u32(&s_bar[kg][0]);
@@ -207,34 +223,19 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     c.s = span_of<TILE>(a, c.b, a.err);
     c.tile = 0;
   } else {
-    int64_t all;
-    atoms_before<TILE>(a, 0, &all, s_scan);
-    all *= HZ;
+    // a stretch of sequences per thread; the one that holds atom `begin` finds it
+    const int32_t per = (a.B + kThreads - 1) / kThreads, b0 = tid * per, b1 = b0 + per < a.B ? b0 + per : a.B;
+    int64_t mine = 0, before;
+    for (int32_t b = b0; b < b1; ++b) mine += atoms_of<TILE>(a, b);
+    const int64_t all = block_scan(mine * HZ, &before, s_scan);
     const int64_t share = share_of(a, all), begin = (int64_t)blockIdx.x * share;
     c.left = all - begin < share ? all - begin : share;
     if (c.left <= 0) return;
-    if (warp == 0) {   // the sequence that holds atom `begin`
-      int64_t base = 0;
-      for (int32_t b0 = 0; b0 < a.B; b0 += 32) {
-        int64_t t = 0;
-        if (b0 + lane < a.B)
-          t = (int64_t)((span_of<TILE>(a, b0 + lane, nullptr).tiles + a.atom - 1) / a.atom) * HZ;
-        int64_t up = t;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
-          if (lane >= o) up += v;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, base + up > begin);
-        if (hit) {
-          if (lane == __ffs(hit) - 1) {
-            s_first[0] = b0 + lane;
-            s_first[1] = begin - (base + up - t);
-          }
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, up, 31);
-      }
+    if (begin >= before && begin < before + mine * HZ) {
+      int32_t b = b0;
+      for (int64_t n; b + 1 < b1 && before + (n = atoms_of<TILE>(a, b) * HZ) <= begin; ++b) before += n;
+      s_first[0] = b;
+      s_first[1] = begin - before;
     }
     __syncthreads();
     c.b = (int32_t)s_first[0];
@@ -320,43 +321,48 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   for (int i = 0; i < S - 1; ++i) rows_q[i] = p_live ? issue(i) : 0u;
 
   // ---- segments -------------------------------------------------------------------
+  // Scores are K Q^T and outputs V^T P^T: keys (then dims) on the 16 rows of an
+  // mma, 8 heads on its columns, so up to 8 heads cost half of what 16 do.  A
+  // lane holds keys g, g + 8 (dims g, g + 8 of each 16) of heads 2 t4, 2 t4 + 1
+  // of each block of 8.
   int st = 0;   // ring slot of the current step
   uint32_t phase = 0;
   bool dead = false;   // a wait ran out: no more waiting, the result is void
   const int kmat = lane >> 3, kr = lane & 7;
-  // ldmatrix rows: keys in non-transposed pairs (dims lo, hi of 8 keys), values in
-  // transposed ones (keys 0-7, 8-15 of 8 dims)
-  const uint32_t k_lane = (kr + (kmat >> 1) * 8) * 128 + (((kmat & 1) ^ kr) << 4);
-  const uint32_t v_lane = BOXES * BOX + (kr + (kmat & 1) * 8) * 128 + (((kmat >> 1) ^ kr) << 4);
+  // ldmatrix rows: keys as (keys 0-7, 8-15) x (dims lo, hi), values transposed as
+  // (dims lo, hi) x (keys 0-7, 8-15)
+  const uint32_t k_lane = (kr + (kmat & 1) * 8) * 128 + (((kmat >> 1) ^ kr) << 4);
+  const uint32_t v_lane = BOXES * BOX + (kr + (kmat >> 1) * 8) * 128 + (((kmat & 1) ^ kr) << 4);
   for (bool more = true; more;) {
     const int kvh = c.hz / blocks, hb = c.hz - kvh * blocks;
-    const int h_lo = hb * 16 * WH + wh * 16 + g;    // heads of the group that this lane's rows are
-    const int h_hi = h_lo + 8;
-    const int64_t hq = (int64_t)kvh * G;
-    uint32_t q[DP / 16][4];
-    {
-      const char* const q_lo = a.q + c.b * a.q_token + (hq + h_lo) * a.q_head;
-      const char* const q_hi = q_lo + 8 * a.q_head;
+    const int h0 = hb * HEADS + wh * (8 * NB);   // first head of the warp, in the group
+    const int64_t hq = (int64_t)kvh * G, bh = (int64_t)c.b * a.H + hq;
+    uint32_t q[NB][DP / 16][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int h = h0 + nb * 8 + g;
+      const char* const qh = a.q + c.b * a.q_token + (hq + h) * a.q_head + 4 * t4;
 #pragma unroll
       for (int ks = 0; ks < DP / 16; ++ks) {
-        const int d0 = ks * 16 + 2 * t4;
-        q[ks][0] = h_lo < G && d0 < a.d ? *reinterpret_cast<const uint32_t*>(q_lo + 2 * d0) : 0u;
-        q[ks][1] = h_hi < G && d0 < a.d ? *reinterpret_cast<const uint32_t*>(q_hi + 2 * d0) : 0u;
-        q[ks][2] = h_lo < G && d0 + 8 < a.d ? *reinterpret_cast<const uint32_t*>(q_lo + 2 * d0 + 16) : 0u;
-        q[ks][3] = h_hi < G && d0 + 8 < a.d ? *reinterpret_cast<const uint32_t*>(q_hi + 2 * d0 + 16) : 0u;
+        q[nb][ks][0] = h < G && ks * 16 < a.d ? *reinterpret_cast<const uint32_t*>(qh + ks * 32) : 0u;
+        q[nb][ks][1] = h < G && ks * 16 + 8 < a.d ? *reinterpret_cast<const uint32_t*>(qh + ks * 32 + 16) : 0u;
       }
     }
-    float o[DP / 8][4];
+    float o[NB][DP / 16][4];
 #pragma unroll
-    for (int i = 0; i < DP / 8; ++i)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+      for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nb][i][j] = 0.f;
     // running maxima (of scaled scores, base 2) and this lane's part of the sums
-    float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb][0] = m[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.f;
+    }
     const int32_t first_tile = c.tile;
-    float* sc = nullptr;
-    if (a.scores != nullptr)
-      sc = a.scores + (c.b * (int64_t)a.H + hq + h_lo) * a.score_stride + c.s.start + c.tile * TILE + kg * kKeys + 2 * t4;
     for (; c.tile < c.end; ++c.tile) {
       if (!dead && !mbar_wait(bars + 8 * st, phase)) {
         dead = true;
@@ -373,28 +379,30 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         phase ^= 1u;
       }
 
-      float sa[2][4] = {}, sb[2][4] = {};   // even and odd k-steps: shorter chains
+      float s[NB][2][4] = {};   // even and odd k-steps: shorter chains
 #pragma unroll
       for (int ks = 0; ks < DP / 16; ks += 2) {
-        uint32_t k0[4], k1[4];
-        ldmatrix_x4(k0, base + (ks >> 2) * BOX + (k_lane ^ ((ks & 3) * 32)));
-        ldmatrix_x4(k1, base + (ks >> 2) * BOX + (k_lane ^ ((ks & 3) * 32 + 32)));
-        mma16816<T>(sa[0], q[ks], k0[0], k0[1]);
-        mma16816<T>(sa[1], q[ks], k0[2], k0[3]);
-        mma16816<T>(sb[0], q[ks + 1], k1[0], k1[1]);
-        mma16816<T>(sb[1], q[ks + 1], k1[2], k1[3]);
+        if (ks * 16 < a.d) {
+          uint32_t k0[4], k1[4];
+          ldmatrix_x4(k0, base + (ks >> 2) * BOX + (k_lane ^ ((ks & 3) * 32)));
+          ldmatrix_x4(k1, base + (ks >> 2) * BOX + (k_lane ^ ((ks & 3) * 32 + 32)));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma16816<T>(s[nb][0], k0, q[nb][ks][0], q[nb][ks][1]);
+            mma16816<T>(s[nb][1], k1, q[nb][ks + 1][0], q[nb][ks + 1][1]);
+          }
+        }
       }
-      float s[2][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = (sa[nt][j] + sb[nt][j]) * a.scale;
+        for (int j = 0; j < 4; ++j) s[nb][0][j] = (s[nb][0][j] + s[nb][1][j]) * a.scale;
       if (rows != 0xffffu) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (!((rows >> (nt * 8 + 2 * t4 + (j & 1))) & 1u)) s[nt][j] = -INFINITY;
+            if (!((rows >> (g + (j >> 1) * 8)) & 1u)) s[nb][0][j] = -INFINITY;
         // 0 times what lies in an unseen value row may be NaN: clear those rows
         // (every warp of the group all of them, so that none waits for another)
         for (int i = lane; i < kKeys * BOXES * 8; i += 32) {
@@ -406,202 +414,215 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         __syncwarp();
       }
       if (a.scores != nullptr) {
-        const int32_t s0 = c.s.start + c.tile * TILE + kg * kKeys + 2 * t4;
+        const int32_t s0 = c.s.start + c.tile * TILE + kg * kKeys + g;
+        float* const sc = a.scores + (bh + h0 + 2 * t4) * a.score_stride + s0;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          if (s0 + nt * 8 < c.s.n) {   // rows hold an even number of slots
-            if (h_lo < G) *reinterpret_cast<float2*>(sc + nt * 8) = make_float2(s[nt][0], s[nt][1]);
-            if (h_hi < G) *reinterpret_cast<float2*>(sc + 8 * a.score_stride + nt * 8) = make_float2(s[nt][2], s[nt][3]);
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (s0 + (j >> 1) * 8 < c.s.n && h0 + nb * 8 + 2 * t4 + (j & 1) < G)
+              sc[(nb * 8 + (j & 1)) * a.score_stride + (j >> 1) * 8] = s[nb][0][j];
+      }
+      bool grows = false;
+      float x[NB][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[nb][e] = fmaxf(s[nb][0][e], s[nb][0][e + 2]);
+          grows |= x[nb][e] > m[nb][e];
+        }
+      if (__any_sync(0xffffffffu, grows)) {   // some head's maximum grows
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = x[nb][e];
+#pragma unroll
+            for (int off = 4; off <= 16; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+            const float top = fmaxf(m[nb][e], v);
+            const float f = top == -INFINITY ? 1.f : ex2(m[nb][e] - top);
+            m[nb][e] = top;
+            l[nb][e] *= f;
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+              o[nb][i][e] *= f;
+              o[nb][i][e + 2] *= f;
+            }
           }
-        }
-        sc += TILE;
       }
-      float x_lo = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      float x_hi = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-      if (__any_sync(0xffffffffu, x_lo > m_lo || x_hi > m_hi)) {   // some row's maximum grows
+      uint32_t pb[NB][2];
 #pragma unroll
-        for (int off = 1; off <= 2; off <<= 1) {
-          x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, off));
-          x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, off));
-        }
-        const float n_lo = fmaxf(m_lo, x_lo), n_hi = fmaxf(m_hi, x_hi);
-        const float f_lo = n_lo == -INFINITY ? 1.f : ex2(m_lo - n_lo);
-        const float f_hi = n_hi == -INFINITY ? 1.f : ex2(m_hi - n_hi);
-        m_lo = n_lo;
-        m_hi = n_hi;
-        l_lo *= f_lo;
-        l_hi *= f_hi;
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          o[i][0] *= f_lo;
-          o[i][1] *= f_lo;
-          o[i][2] *= f_hi;
-          o[i][3] *= f_hi;
-        }
-      }
-      const float r_lo = m_lo == -INFINITY ? 0.f : m_lo, r_hi = m_hi == -INFINITY ? 0.f : m_hi;
-      uint32_t pa[4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const float p0 = ex2(s[nt][0] - r_lo), p1 = ex2(s[nt][1] - r_lo);
-        const float p2 = ex2(s[nt][2] - r_hi), p3 = ex2(s[nt][3] - r_hi);
-        l_lo += p0 + p1;
-        l_hi += p2 + p3;
-        pa[2 * nt] = pack2<T>(p0, p1);
-        pa[2 * nt + 1] = pack2<T>(p2, p3);
+      for (int nb = 0; nb < NB; ++nb) {
+        const float r0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], r1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
+        const float p0 = ex2(s[nb][0][0] - r0), p1 = ex2(s[nb][0][1] - r1);
+        const float p2 = ex2(s[nb][0][2] - r0), p3 = ex2(s[nb][0][3] - r1);
+        l[nb][0] += p0 + p2;
+        l[nb][1] += p1 + p3;
+        // (key, 2 heads) to (head, 2 keys)
+        pb[nb][0] = transpose8x8(pack2<T>(p0, p1));
+        pb[nb][1] = transpose8x8(pack2<T>(p2, p3));
       }
 #pragma unroll
       for (int j = 0; j < DP / 16; ++j) {
-        uint32_t vb[4];
-        ldmatrix_x4_trans(vb, base + (j >> 2) * BOX + (v_lane ^ ((j & 3) * 32)));
-        mma16816<T>(o[2 * j], pa, vb[0], vb[1]);
-        mma16816<T>(o[2 * j + 1], pa, vb[2], vb[3]);
+        if (j * 16 < a.d) {
+          uint32_t va[4];
+          ldmatrix_x4_trans(va, base + (j >> 2) * BOX + (v_lane ^ ((j & 3) * 32)));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816<T>(o[nb][j], va, pb[nb][0], pb[nb][1]);
+        }
       }
     }
 
     // ---- join the key groups, store --------------------------------------------
     // Everyone has read slot st - 1 to the end; the next step fills it.
 #pragma unroll
-    for (int off = 1; off <= 2; off <<= 1) {
-      l_lo += __shfl_xor_sync(0xffffffffu, l_lo, off);
-      l_hi += __shfl_xor_sync(0xffffffffu, l_hi, off);
-    }
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], off);
     const bool whole_unit = first_tile == 0 && c.tile == c.s.tiles;   // no other piece exists
-    const int64_t bh = (int64_t)c.b * a.H + hq;
     const int64_t piece = a.invariant ? ((int64_t)c.b * HZ + c.hz) * a.max_atoms + first_tile / a.atom
                                       : 2 * (int64_t)blockIdx.x + (continued ? 0 : 1);
-    // Stores 4 (or 2) neighbouring columns of a row of heads.
-    auto store_ml = [&](int row, float m, float l) {   // row: of the head block
-      const int h = hb * 16 * WH + row;
+    const int prev = st == 0 ? S - 1 : st - 1;
+    auto sink_of = [&](int h) { return a.sink && h < G ? a.sink[hq + h] * kLog2e : -INFINITY; };
+    auto store_ml = [&](int row, float top, float sum) {   // row: of the unit's heads
+      const int h = hb * HEADS + row;
       if (!whole_unit) {
-        *reinterpret_cast<float2*>(a.part_ml + (piece * (16 * WH) + row) * 2) = make_float2(m, l);
+        *reinterpret_cast<float2*>(a.part_ml + (piece * HEADS + row) * 2) = make_float2(top, sum);
       } else if (h < G) {
-        const Norm nm = normalise(m, l, a.sink ? a.sink[hq + h] * kLog2e : -INFINITY);
+        const Norm nm = normalise(top, sum, sink_of(h));
         if (a.lse) a.lse[bh + h] = nm.lse2 * (1.f / kLog2e);
         if (a.lse2) a.lse2[bh + h] = nm.lse2;
       }
     };
+    if constexpr (NG > 1) {
+      if (g == 0) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) s_ml[kg][wh * (8 * NB) + nb * 8 + 2 * t4 + e] = make_float2(m[nb][e], l[nb][e]);
+      }
+    }
     if constexpr (NG == 4) {
-      // every warp puts its O down and sums a quarter of the columns of all four
-      const int prev = st == 0 ? S - 1 : st - 1;
+      // every warp puts its O down, [head][dim], and sums a quarter of the columns of all four
       float* const mine = reinterpret_cast<float*>(smem + (kg * S + prev) * Geo::STAGE);
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < DP / 8; ++i) {
-        // 8-float blocks permuted by row, off the bank conflicts
-        const int at = ((i ^ (g & 3)) * 8) + 2 * t4;
-        *reinterpret_cast<float2*>(mine + g * DP + at) = make_float2(o[i][0], o[i][1]);
-        *reinterpret_cast<float2*>(mine + (g + 8) * DP + at) = make_float2(o[i][2], o[i][3]);
-      }
-      if (t4 == 0) {
-        s_ml[warp][g] = make_float2(m_lo, l_lo);
-        s_ml[warp][g + 8] = make_float2(m_hi, l_hi);
-      }
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)   // 8-float blocks permuted by head pair, off the bank conflicts
+            mine[(nb * 8 + 2 * t4 + (j & 1)) * DP + ((i * 16 + (j >> 1) * 8 + g) ^ (t4 * 8))] = o[nb][i][j];
       __syncthreads();
       constexpr int F4 = DP / 16;   // float4 per row of a quarter
 #pragma unroll
-      for (int i = 0; i < 16 * F4 / 32; ++i) {
+      for (int i = 0; i < HEADS * F4 / 32; ++i) {
         const int idx = i * 32 + lane, row = idx / F4, col = warp * (DP / 4) + (idx % F4) * 4;
-        float m = -INFINITY, l = 0.f;
+        float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) m = fmaxf(m, s_ml[w][row].x);
-        const float R = m == -INFINITY ? 0.f : m;
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, s_ml[w][row].x);
+        const float R = top == -INFINITY ? 0.f : top;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const float2 ml = s_ml[w][row];
           const float f = ex2(ml.x - R);
-          l = fmaf(ml.y, f, l);
-          const float4 x = *reinterpret_cast<const float4*>(
-              reinterpret_cast<const float*>(smem + (w * S + prev) * Geo::STAGE) + row * DP + (col ^ ((row & 3) * 8)));
-          acc.x = fmaf(x.x, f, acc.x);
-          acc.y = fmaf(x.y, f, acc.y);
-          acc.z = fmaf(x.z, f, acc.z);
-          acc.w = fmaf(x.w, f, acc.w);
+          sum = fmaf(ml.y, f, sum);
+          const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + (w * S + prev) * Geo::STAGE) +
+                                                            row * DP + (col ^ (((row >> 1) & 3) * 8)));
+          acc.x = fmaf(y.x, f, acc.x);
+          acc.y = fmaf(y.y, f, acc.y);
+          acc.z = fmaf(y.z, f, acc.z);
+          acc.w = fmaf(y.w, f, acc.w);
         }
-        const int h = hb * 16 + row;
+        const int h = hb * HEADS + row;
         if (whole_unit) {
           if (h < G && col < a.d) {
-            const float k = normalise(m, l, a.sink ? a.sink[hq + h] * kLog2e : -INFINITY).scale;
+            const float k = normalise(top, sum, sink_of(h)).scale;
             uint2 pk;
             pk.x = pack2<T>(acc.x * k, acc.y * k);
             pk.y = pack2<T>(acc.z * k, acc.w * k);
             *reinterpret_cast<uint2*>(a.out + ((bh + h) * a.d + col) * 2) = pk;
           }
         } else {
-          *reinterpret_cast<float4*>(a.part_acc + (piece * 16 + row) * DP + col) = acc;
+          *reinterpret_cast<float4*>(a.part_acc + (piece * HEADS + row) * DP + col) = acc;
         }
-        if (col == 0) store_ml(row, m, l);
+        if (col == 0) store_ml(row, top, sum);
       }
       fence_async_smem_cta();
       __syncthreads();   // the slots may be filled again
     } else {
       if constexpr (NG == 2) {   // group 1 hands its O to group 0 through both groups' slots
-        const int prev = st == 0 ? S - 1 : st - 1;
-        float2* const buf = reinterpret_cast<float2*>(smem + (wh * S + prev) * Geo::STAGE) + lane;
-        if (t4 == 0) {
-          s_ml[warp][g] = make_float2(m_lo, l_lo);
-          s_ml[warp][g + 8] = make_float2(m_hi, l_hi);
-        }
+        float4* const buf = reinterpret_cast<float4*>(smem + (wh * S + prev) * Geo::STAGE) + lane;
         __syncthreads();   // and both groups have left their slots
-        const float2 x_lo = s_ml[(1 - kg) * WH + wh][g], x_hi = s_ml[(1 - kg) * WH + wh][g + 8];
-        const float M_lo = fmaxf(m_lo, x_lo.x), M_hi = fmaxf(m_hi, x_hi.x);
-        const float R_lo = M_lo == -INFINITY ? 0.f : M_lo, R_hi = M_hi == -INFINITY ? 0.f : M_hi;
-        const float f_lo = ex2(m_lo - R_lo), f_hi = ex2(m_hi - R_hi);
-        l_lo = l_lo * f_lo + x_lo.y * ex2(x_lo.x - R_lo);
-        l_hi = l_hi * f_hi + x_hi.y * ex2(x_hi.x - R_hi);
-        m_lo = M_lo;
-        m_hi = M_hi;
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          o[i][0] *= f_lo;
-          o[i][1] *= f_lo;
-          o[i][2] *= f_hi;
-          o[i][3] *= f_hi;
-          if (kg == 1) {
-            buf[(2 * i) * 32] = make_float2(o[i][0], o[i][1]);
-            buf[(2 * i + 1) * 32] = make_float2(o[i][2], o[i][3]);
+        for (int nb = 0; nb < NB; ++nb) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 other = s_ml[1 - kg][wh * (8 * NB) + nb * 8 + 2 * t4 + e];
+            const float top = fmaxf(m[nb][e], other.x), R = top == -INFINITY ? 0.f : top;
+            f[e] = ex2(m[nb][e] - R);
+            l[nb][e] = l[nb][e] * f[e] + other.y * ex2(other.x - R);
+            m[nb][e] = top;
+          }
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i) {
+            o[nb][i][0] *= f[0];
+            o[nb][i][1] *= f[1];
+            o[nb][i][2] *= f[0];
+            o[nb][i][3] *= f[1];
+            if (kg == 1) buf[(nb * (DP / 16) + i) * 32] = make_float4(o[nb][i][0], o[nb][i][1], o[nb][i][2], o[nb][i][3]);
           }
         }
         __syncthreads();
         if (kg == 0) {
 #pragma unroll
-          for (int i = 0; i < DP / 8; ++i) {
-            const float2 x = buf[(2 * i) * 32], y = buf[(2 * i + 1) * 32];
-            o[i][0] += x.x;
-            o[i][1] += x.y;
-            o[i][2] += y.x;
-            o[i][3] += y.y;
-          }
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+              const float4 y = buf[(nb * (DP / 16) + i) * 32];
+              o[nb][i][0] += y.x;
+              o[nb][i][1] += y.y;
+              o[nb][i][2] += y.z;
+              o[nb][i][3] += y.w;
+            }
         }
         fence_async_smem_cta();
         __syncthreads();
       }
       if (kg == 0) {
-        const int row = wh * 16 + g;
-        if (t4 == 0) {
-          store_ml(row, m_lo, l_lo);
-          store_ml(row + 8, m_hi, l_hi);
-        }
-        if (whole_unit) {
-          const float k_lo = h_lo < G ? normalise(m_lo, l_lo, a.sink ? a.sink[hq + h_lo] * kLog2e : -INFINITY).scale : 0.f;
-          const float k_hi = h_hi < G ? normalise(m_hi, l_hi, a.sink ? a.sink[hq + h_hi] * kLog2e : -INFINITY).scale : 0.f;
-          char* const out_lo = a.out + (bh + h_lo) * a.d * 2;
-          char* const out_hi = out_lo + 8 * a.d * 2;
 #pragma unroll
-          for (int i = 0; i < DP / 8; ++i) {
-            const int d0 = i * 8 + 2 * t4;
-            if (d0 < a.d) {
-              if (h_lo < G) *reinterpret_cast<uint32_t*>(out_lo + 2 * d0) = pack2<T>(o[i][0] * k_lo, o[i][1] * k_lo);
-              if (h_hi < G) *reinterpret_cast<uint32_t*>(out_hi + 2 * d0) = pack2<T>(o[i][2] * k_hi, o[i][3] * k_hi);
-            }
+        for (int nb = 0; nb < NB; ++nb) {
+          const int row = wh * (8 * NB) + nb * 8 + 2 * t4;   // and row + 1
+          if (g == 0) {
+            store_ml(row, m[nb][0], l[nb][0]);
+            store_ml(row + 1, m[nb][1], l[nb][1]);
           }
-        } else {
-          float* const acc = a.part_acc + (piece * (16 * WH) + row) * DP;
+          if (whole_unit) {
+            const int h = hb * HEADS + row + (g & 1);
+            const float k0 = normalise(m[nb][0], l[nb][0], sink_of(hb * HEADS + row)).scale;
+            const float k1 = normalise(m[nb][1], l[nb][1], sink_of(hb * HEADS + row + 1)).scale;
+            char* const out = a.out + ((bh + h) * a.d + (g & 6)) * 2;
 #pragma unroll
-          for (int i = 0; i < DP / 8; ++i) {
-            *reinterpret_cast<float2*>(acc + i * 8 + 2 * t4) = make_float2(o[i][0], o[i][1]);
-            *reinterpret_cast<float2*>(acc + 8 * DP + i * 8 + 2 * t4) = make_float2(o[i][2], o[i][3]);
+            for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {   // lanes of dims g, g ^ 1 trade heads for neighbours
+                const float v0 = o[nb][i][2 * half] * k0, v1 = o[nb][i][2 * half + 1] * k1;
+                const float y = __shfl_xor_sync(0xffffffffu, (g & 1) ? v0 : v1, 4);
+                const int d0 = i * 16 + half * 8;
+                if (h < G && d0 < a.d)
+                  *reinterpret_cast<uint32_t*>(out + 2 * d0) = (g & 1) ? pack2<T>(y, v1) : pack2<T>(v0, y);
+              }
+          } else {
+            float* const acc = a.part_acc + (piece * HEADS + row) * DP + g;
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[(j & 1) * DP + i * 16 + (j >> 1) * 8] = o[nb][i][j];
           }
         }
       }
@@ -624,132 +645,152 @@ struct Pieces {
 };
 template <int TILE>
 __device__ Pieces pieces_of(const KvAttnArgs& a, int32_t b, int HZ, int hz, int64_t* scratch) {
-  const int32_t tiles = span_of<TILE>(a, b, nullptr).tiles;
-  const int64_t atoms = (tiles + a.atom - 1) / a.atom;
-  Pieces r;
+  const int64_t atoms = atoms_of<TILE>(a, b);
   if (a.invariant) {
-    r.first = ((int64_t)b * HZ + hz) * a.max_atoms;
-    r.second = r.first + 1;
-    r.count = atoms;
-    r.step = 1;
-    return r;
+    const int64_t first = ((int64_t)b * HZ + hz) * a.max_atoms;
+    return Pieces{first, first + 1, atoms, 1};
   }
-  int64_t all;
-  const int64_t base = atoms_before<TILE>(a, b, &all, scratch) * HZ + hz * atoms;
+  int64_t mine = 0, low = 0, x;
+  for (int32_t i = threadIdx.x; i < a.B; i += kThreads) {
+    const int64_t n = atoms_of<TILE>(a, i);
+    mine += n;
+    if (i < b) low += n;
+  }
+  const int64_t all = block_scan(mine, &x, scratch), base = block_scan(low, &x, scratch) * HZ + hz * atoms;
+  if (atoms == 0) return Pieces{0, 0, 0, 2};
   const int64_t share = share_of(a, all * HZ);
-  if (atoms == 0) {
-    r.first = r.second = r.count = 0;
-    r.step = 2;
-    return r;
-  }
   const int64_t c0 = base / share, c1 = (base + atoms - 1) / share;
-  r.first = 2 * c0 + 1;   // it begins in c0's run; the others' runs begin in it
-  r.second = 2 * (c0 + 1);
-  r.count = c1 - c0 + 1;
-  r.step = 2;
-  return r;
+  return Pieces{2 * c0 + 1, 2 * (c0 + 1), c1 - c0 + 1, 2};   // it begins in c0's run; the others' runs begin in it
 }
 
-constexpr int kWeighSlots = 1024;   // slots of a weighing block
+// (max, sum) of two parts of one softmax.
+__device__ __forceinline__ float2 join_ml(float2 x, float2 y) {
+  const float M = fmaxf(x.x, y.x), R = M == -INFINITY ? 0.f : M;
+  return make_float2(M, x.y * ex2(x.x - R) + y.y * ex2(y.x - R));
+}
 
-// Blocks x < join_blocks: one warp per head joins that head's pieces (count 1:
-// the attention kernel has written the result; 0: an empty sequence).  The
-// others, with weights_out: the log-sum-exps of the group from the pieces,
-// then the probabilities of the scores, summed over the group in head order.
-template <class T, int DP, int WH>
-__global__ void __launch_bounds__(kThreads) kv_finish_kernel(KvAttnArgs a, int join_blocks) {
-  constexpr int TILE = Geometry<T, DP, WH>::TILE, ROWS = 16 * WH;
-  __shared__ int64_t s_scan[8];
-  __shared__ float s_lse[128];
-  pdl_wait();
-  pdl_trigger();
+// Joins the pieces of the units that have several (or none: an empty
+// sequence; the attention kernel has written the others).  `split` of the
+// block's four warps share a head's pieces.
+template <class T, int DP, int NB, int WH>
+__global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ KvAttnArgs a, int split) {
+  using Geo = Geometry<T, DP, NB, WH>;
+  constexpr int ROWS = Geo::HEADS, V = DP / 64;   // float2 per lane
+  __shared__ int64_t s_scan[4];
+  __shared__ float2 s_ml[4];
+  __shared__ float2 s_acc[4][V][32];
   const int b = blockIdx.z, kvh = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.H / a.n_kv_heads, blocks = (G + ROWS - 1) / ROWS, HZ = a.n_kv_heads * blocks;
-  const int64_t bh = (int64_t)b * a.H + (int64_t)kvh * G;
-
-  if ((int)blockIdx.x < join_blocks) {
-    if (a.whole) return;
-    const int h = blockIdx.x * 4 + warp;
-    const int hb = (blockIdx.x * 4) / ROWS;   // 4 divides the heads of a block
-    const Pieces ps = pieces_of<TILE>(a, b, HZ, kvh * blocks + hb, s_scan);
-    if (h >= G || ps.count == 1) return;
-    const int row = h - hb * ROWS;
-    const float z = a.sink ? a.sink[kvh * G + h] * kLog2e : -INFINITY;
-    float M = z;
-    for (int64_t i = lane; i < ps.count; i += 32) M = fmaxf(M, a.part_ml[(ps.at(i) * ROWS + row) * 2]);
+  const int first = blockIdx.x * (4 / split);   // 4 / split heads, in one head block
+  const int hb = first / ROWS;
+  // the lengths do not come from the attention kernel: read them while it runs
+  const Pieces ps = pieces_of<Geo::TILE>(a, b, HZ, kvh * blocks + hb, s_scan);
+  pdl_wait();
+  pdl_trigger();
+  if (ps.count == 1) return;
+  const int h = first + warp / split, part = warp % split, row = h - hb * ROWS;
+  float2 ml = make_float2(-INFINITY, 0.f);
+  float2 acc[V];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float R = M == -INFINITY ? 0.f : M;
-    float den = z == -INFINITY ? 0.f : exp2f(z - R);
-    float2 acc[DP / 64];
+  for (int j = 0; j < V; ++j) acc[j] = make_float2(0.f, 0.f);
+  if (h < G) {
+    for (int64_t i = part + split * (int64_t)lane; i < ps.count; i += split * 32)
+      ml.x = fmaxf(ml.x, a.part_ml[(ps.at(i) * ROWS + row) * 2]);
 #pragma unroll
-    for (int j = 0; j < DP / 64; ++j) acc[j] = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int64_t i = 0; i < ps.count; ++i) {
+    for (int o = 16; o >= 1; o >>= 1) ml.x = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, o));
+    const float R = ml.x == -INFINITY ? 0.f : ml.x;
+#pragma unroll 8
+    for (int64_t i = part; i < ps.count; i += split) {
       const int64_t at = ps.at(i) * ROWS + row;
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-      const float f = exp2f(ml.x - R);
-      den += ml.y * f;
+      const float2 p = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+      const float f = ex2(p.x - R);
+      ml.y = fmaf(p.y, f, ml.y);
 #pragma unroll
-      for (int j = 0; j < DP / 64; ++j) {
-        const float2 x = *reinterpret_cast<const float2*>(a.part_acc + at * DP + j * 64 + 2 * lane);
-        acc[j].x = fmaf(x.x, f, acc[j].x);
-        acc[j].y = fmaf(x.y, f, acc[j].y);
+      for (int j = 0; j < V; ++j) {
+        const float2 y = *reinterpret_cast<const float2*>(a.part_acc + at * DP + j * 64 + 2 * lane);
+        acc[j].x = fmaf(y.x, f, acc[j].x);
+        acc[j].y = fmaf(y.y, f, acc[j].y);
       }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-#pragma unroll
-    for (int j = 0; j < DP / 64; ++j)
-      if (j * 64 + 2 * lane < a.d)
-        *reinterpret_cast<uint32_t*>(a.out + ((bh + h) * a.d + j * 64 + 2 * lane) * 2) =
-            pack2<T>(acc[j].x * inv, acc[j].y * inv);
-    if (lane == 0 && a.lse) a.lse[bh + h] = den == 0.f ? -INFINITY : (R + log2f(den)) * (1.f / kLog2e);
-    return;
   }
-
-  const int32_t n = kv_clamp_len(__ldg(a.lens + b), a.max_len, b, nullptr);
-  const int32_t s0 = (blockIdx.x - join_blocks) * kWeighSlots;
-  if (s0 >= n) return;
-  for (int hb = 0; hb < blocks; ++hb) {
-    Pieces ps{0, 0, 1, 1};
-    if (!a.whole) ps = pieces_of<TILE>(a, b, HZ, kvh * blocks + hb, s_scan);
-    const int end = G - hb * ROWS < ROWS ? G - hb * ROWS : ROWS;
-    for (int r = warp; r < end; r += 4) {
-      const int h = hb * ROWS + r;
-      float e;
-      if (ps.count == 1) {
-        e = a.lse2[bh + h];
-      } else {
-        const float z = a.sink ? a.sink[kvh * G + h] * kLog2e : -INFINITY;
-        float M = z;
-        for (int64_t i = lane; i < ps.count; i += 32) M = fmaxf(M, a.part_ml[(ps.at(i) * ROWS + r) * 2]);
+  if (split > 1) {
+    if (lane == 0) s_ml[warp] = ml;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float R = M == -INFINITY ? 0.f : M;
-        float den = 0.f;
-        for (int64_t i = lane; i < ps.count; i += 32) {
-          const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (ps.at(i) * ROWS + r) * 2);
-          den += ml.y * exp2f(ml.x - R);
-        }
+    for (int j = 0; j < V; ++j) s_acc[warp][j][lane] = acc[j];
+    __syncthreads();
+    if (part != 0) return;
+    const float own = ml.x;
+    for (int w = 1; w < split; ++w) ml = join_ml(ml, s_ml[warp + w]);
+    const float R = ml.x == -INFINITY ? 0.f : ml.x, f0 = ex2(own - R);
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-        if (z != -INFINITY) den += exp2f(z - R);
-        e = R + log2f(den);
+    for (int j = 0; j < V; ++j) {
+      acc[j].x *= f0;
+      acc[j].y *= f0;
+      for (int w = 1; w < split; ++w) {
+        const float f = ex2(s_ml[warp + w].x - R);
+        acc[j].x = fmaf(s_acc[warp + w][j][lane].x, f, acc[j].x);
+        acc[j].y = fmaf(s_acc[warp + w][j][lane].y, f, acc[j].y);
       }
-      // a head without any weight (every slot on a bad page) adds nothing
-      if (lane == 0) s_lse[h] = e == -INFINITY ? INFINITY : e;
     }
+  }
+  if (h >= G) return;
+  const int64_t bh = (int64_t)b * a.H + (int64_t)kvh * G + h;
+  const Norm nm = normalise(ml.x, ml.y, a.sink ? a.sink[kvh * G + h] * kLog2e : -INFINITY);
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (j * 64 + 2 * lane < a.d)
+      *reinterpret_cast<uint32_t*>(a.out + (bh * a.d + j * 64 + 2 * lane) * 2) = pack2<T>(acc[j].x * nm.scale, acc[j].y * nm.scale);
+  if (lane == 0) {
+    if (a.lse) a.lse[bh] = nm.lse2 * (1.f / kLog2e);
+    if (a.lse2) a.lse2[bh] = nm.lse2;
+  }
+}
+
+// weights_out: the probabilities of the scores, summed over the group.  128
+// slots at a time, four to a lane; the four warps take the group's heads apart
+// and their sums are added in warp order.
+__global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const __grid_constant__ KvAttnArgs a, int slots_per_block) {
+  __shared__ float s_lse[128];
+  __shared__ float4 s_sum[4][32];
+  const int b = blockIdx.z, kvh = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.H / a.n_kv_heads;
+  const int64_t bh = (int64_t)b * a.H + (int64_t)kvh * G;
+  const int32_t n = kv_clamp_len(__ldg(a.lens + b), a.max_len, b, nullptr);
+  const int32_t s0 = blockIdx.x * slots_per_block;
+  pdl_wait();
+  pdl_trigger();
+  if (s0 >= n) return;
+  if (tid < G) {   // a head without any weight (every slot on a bad page) adds nothing
+    const float e = a.lse2[bh + tid];
+    s_lse[tid] = e == -INFINITY ? INFINITY : e;
   }
   __syncthreads();
-  const float* const sc = a.scores + bh * a.score_stride;
   const int64_t at = ((int64_t)b * a.n_kv_heads + kvh) * a.slots;
-  const int32_t end = s0 + kWeighSlots < n ? s0 + kWeighSlots : n;
-  for (int32_t s = s0 + threadIdx.x; s < end; s += kThreads) {
-    float w = 0.f;
+  const int32_t end = s0 + slots_per_block < n ? s0 + slots_per_block : n;
+  for (int32_t s = s0; s < end; s += 128) {
+    const float* const sc = a.scores + bh * a.score_stride + s + 4 * lane;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s + 4 * lane < end) {   // a row of scores ends on a multiple of 4
 #pragma unroll 8
-    for (int h = 0; h < G; ++h) w += exp2f(sc[h * a.score_stride + s] - s_lse[h]);
-    a.weights_out[at + s] = a.weights ? a.weights[at + s] + w : w;
+      for (int h = warp; h < G; h += 4) {
+        const float4 z = *reinterpret_cast<const float4*>(sc + h * a.score_stride);
+        const float e = s_lse[h];
+        w.x += ex2(z.x - e);
+        w.y += ex2(z.y - e);
+        w.z += ex2(z.z - e);
+        w.w += ex2(z.w - e);
+      }
+    }
+    s_sum[warp][lane] = w;
+    __syncthreads();
+    if (s + tid < end) {
+      const float* const sum = reinterpret_cast<const float*>(s_sum);
+      const float v = (sum[tid] + sum[128 + tid]) + (sum[256 + tid] + sum[384 + tid]);
+      a.weights_out[at + s + tid] = a.weights ? a.weights[at + s + tid] + v : v;
+    }
+    __syncthreads();
   }
 }
 
@@ -769,34 +810,44 @@ bool tile_map(const char* data, int64_t page_st, int64_t slot_st, int64_t head_s
   return make_tmap_16bit_4d(map, data, dims, strides, 64, kKeys);
 }
 
-template <class T, int DP, int WH>
+template <class T, int DP, int NB, int WH>
 cudaError_t launch_typed(const Launch& L, const KvAttnArgs& args, const KvAttnPlan& p) {
-  using Geo = Geometry<T, DP, WH>;
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<T, DP, WH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::SMEM);
+  using Geo = Geometry<T, DP, NB, WH>;
+  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<T, DP, NB, WH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::SMEM);
   if (e != cudaSuccess) return e;
   KvAttnArgs a = args;
   CUtensorMap map_k = {}, map_v = {};
   a.tiled = tile_map(a.kv.k, a.kv.k_page, a.kv.k_slot, a.kv.k_head, a, &map_k) &&
             tile_map(a.kv.v, a.kv.v_page, a.kv.v_slot, a.kv.v_head, a, &map_v);
   L.begin(kKernelAttention);
-  e = launch_kernel(kv_attn_kernel<T, DP, WH>, dim3((unsigned)p.n_ctas), dim3(kThreads), Geo::SMEM, L.stream, true, map_k,
+  e = launch_kernel(kv_attn_kernel<T, DP, NB, WH>, dim3((unsigned)p.n_ctas), dim3(kThreads), Geo::SMEM, L.stream, true, map_k,
                     map_v, a);
   if (e != cudaSuccess) return e;
   e = L.end(kKernelAttention);
-  if (e != cudaSuccess || (p.whole && a.weights_out == nullptr)) return e;
+  if (e != cudaSuccess || p.whole) return e;
   const int G = a.H / a.n_kv_heads;
-  const int join = p.whole ? 0 : (G + 3) / 4;
-  const int weigh = a.weights_out ? (int)((a.max_len + kWeighSlots - 1) / kWeighSlots) : 0;
+  const int split = (int64_t)a.B * a.n_kv_heads * p.blocks * 4 > p.n_ctas ? 1 : 4;   // 4 where a unit has many pieces
   L.begin(kKernelMerge);
-  e = launch_kernel(kv_finish_kernel<T, DP, WH>, dim3((unsigned)(join + weigh), (unsigned)a.n_kv_heads, (unsigned)a.B),
-                    dim3(kThreads), 0, L.stream, true, a, join);
+  e = launch_kernel(kv_join_kernel<T, DP, NB, WH>, dim3((unsigned)((G * split + 3) / 4), (unsigned)a.n_kv_heads, (unsigned)a.B),
+                    dim3(kThreads), 0, L.stream, true, a, split);
+  if (e != cudaSuccess) return e;
+  return L.end(kKernelMerge);
+}
+
+cudaError_t launch_weigh(const Launch& L, const KvAttnArgs& a) {
+  const int G = a.H / a.n_kv_heads;
+  const int per = G <= 8 ? 512 : G <= 16 ? 256 : 128;   // about 16 KB of scores a block
+  L.begin(kKernelMerge);
+  const cudaError_t e = launch_kernel(kv_weigh_kernel, dim3((unsigned)((a.max_len + per - 1) / per), (unsigned)a.n_kv_heads, (unsigned)a.B),
+                                      dim3(kThreads), 0, L.stream, true, a, per);
   if (e != cudaSuccess) return e;
   return L.end(kKernelMerge);
 }
 
 template <class T, int DP>
 cudaError_t launch_wh(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p) {
-  return p.wh == 1 ? launch_typed<T, DP, 1>(L, a, p) : p.wh == 2 ? launch_typed<T, DP, 2>(L, a, p) : launch_typed<T, DP, 4>(L, a, p);
+  if (p.nb == 1) return launch_typed<T, DP, 1, 1>(L, a, p);
+  return p.wh == 1 ? launch_typed<T, DP, 2, 1>(L, a, p) : p.wh == 2 ? launch_typed<T, DP, 2, 2>(L, a, p) : launch_typed<T, DP, 2, 4>(L, a, p);
 }
 template <class T>
 cudaError_t launch_dp(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p) {
@@ -814,8 +865,10 @@ KvAttnPlan kv_attn_plan(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int
                         bool invariant) {
   KvAttnPlan p{};
   const int G = H / n_kv_heads;
+  p.nb = G <= 8 ? 1 : 2;
   p.wh = G <= 16 ? 1 : G <= 32 ? 2 : 4;
-  p.blocks = (G + 16 * p.wh - 1) / (16 * p.wh);
+  p.heads = 8 * p.nb * p.wh;
+  p.blocks = (G + p.heads - 1) / p.heads;
   p.dp = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256;
   p.tile = kKeys * 4 / p.wh;
   const int64_t units = (int64_t)B * n_kv_heads * p.blocks;
@@ -825,7 +878,7 @@ KvAttnPlan kv_attn_plan(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int
   p.atom = invariant ? kInvariantSlots / p.tile : 1;
   p.max_atoms = (tiles + p.atom - 1) / p.atom;
   p.whole = !invariant && tiles <= 4;
-  const int64_t most = (int64_t)kSms * (p.dp <= 128 ? 2 : 1);
+  const int64_t most = (int64_t)kSms * ctas_per_sm(p.dp, p.nb);
   if (p.whole) {
     p.n_ctas = (int)units;
     p.pieces = 0;
@@ -838,7 +891,9 @@ KvAttnPlan kv_attn_plan(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int
 }
 
 cudaError_t launch_kv_attn(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p) {
-  return a.dtype == CSA_KV_FP16 ? launch_dp<__half>(L, a, p) : launch_dp<__nv_bfloat16>(L, a, p);
+  const cudaError_t e = a.dtype == CSA_KV_FP16 ? launch_dp<__half>(L, a, p) : launch_dp<__nv_bfloat16>(L, a, p);
+  if (e != cudaSuccess || a.weights_out == nullptr || a.max_len == 0) return e;
+  return launch_weigh(L, a);
 }
 
 }  // namespace csa
