@@ -425,7 +425,7 @@ struct KvAttnArgs {
   float* scores;                // [B, H, score_stride] scaled scores, base 2 (weights_out only)
   int64_t score_stride;
   int32_t tiled;                // 1: rows come as TMA boxes (set by the launch)
-  int32_t n_ctas;               // CTAs that share the tiles
+  int32_t runs;                 // equal shares that the sequences' tiles are cut into
   int32_t whole;                // 1: one CTA per unit, nothing to join
   int32_t atom;                 // tiles that stay together (batch-invariant: a slice)
   int32_t invariant;
@@ -439,7 +439,7 @@ struct KvAttnPlan {
   int blocks;                   // head blocks of a group
   int dp;                       // padded head dim
   int tile;                     // slots of a tile
-  int n_ctas, whole, atom;
+  int runs, n_ctas, whole, atom;
   int64_t max_atoms, pieces;    // pieces: partial results that may exist
 };
 KvAttnPlan kv_attn_plan(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int64_t max_len, int32_t window,

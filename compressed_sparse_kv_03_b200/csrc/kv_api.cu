@@ -300,7 +300,7 @@ csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv
   a.lse2 = weigh ? reinterpret_cast<float*>(p + l.lse_off) : nullptr;
   a.scores = weigh ? reinterpret_cast<float*>(p + l.score_off) : nullptr;
   a.score_stride = l.score_stride;
-  a.n_ctas = l.plan.n_ctas;
+  a.runs = l.plan.runs;
   a.whole = l.plan.whole;
   a.atom = l.plan.atom;
   a.invariant = batch_invariant();
