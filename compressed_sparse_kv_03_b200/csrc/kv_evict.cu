@@ -8,16 +8,21 @@
 // nearly every kept row (256 slots over a budget of 2048: 2048 rows a head
 // instead of about 256).
 //
-// One cluster of CTAs per (sequence, head).  Each warp owns a run of consecutive
-// slots, so ranks are prefix sums over warps and a ballot within a warp:
+// One cluster of CTAs per (sequence, head), of one CTA where the sequences and
+// heads fill the GPU by themselves.  Each warp owns a run of consecutive slots, so
+// ranks are prefix sums over warps and a ballot within a warp:
 //   1. keys from weights and positions, kept in shared memory while they fit;
 //   2. radix select, 8 bits a pass: a histogram per CTA, summed over the
-//      cluster through distributed shared memory;
-//   3. equal keys ranked by slot; the staying slots above the budget and the
-//      holes below it are numbered in order and listed;
+//      cluster through distributed shared memory, until the bin that holds the
+//      budget-th key is wholly kept, or holds at most 64 keys, which are ranked
+//      directly by (key, slot); only keys with more than 64 equals go through
+//      all four passes and are then ranked by slot;
+//   3. the staying slots above the budget and the holes below it are numbered
+//      in order and listed;
 //   4. all CTAs of the cluster copy the listed rows, 16 bytes a thread.
 // Sources lie at or above the budget and targets below it, so the copies need
-// no order.
+// no order.  Bound by latency (a chain of about five loads and ten barriers)
+// until some hundred rows move, then by HBM.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -29,11 +34,11 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCachedKeys = 24576;   // 96 KB of keys per CTA
 constexpr int kUnroll = 4;              // row pieces in flight per thread
+constexpr int kFew = 64;                // keys of a bin that are ranked directly
+constexpr int kSmemList = 512;          // moves listed in shared memory (clusters of one)
 constexpr uint32_t kHeld = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t slot_key(const KvEvictArgs& a, int64_t at, int32_t newest) {
@@ -43,22 +48,37 @@ __device__ __forceinline__ uint32_t slot_key(const KvEvictArgs& a, int64_t at, i
   return w != w ? kHeld - 1 : score_key(w);   // +inf is below kHeld - 1
 }
 
+template <int WARPS>
 struct Shared {
   uint32_t hist[4][256];
-  int32_t warp_eq[kWarps], warp_hole[kWarps], warp_move[kWarps];
-  int32_t cta_eq, cta_hole, cta_move;
+  int32_t warp_a[WARPS], warp_b[WARPS];
+  int32_t cta_a, cta_b;
   uint32_t bin, above, count;
+  uint32_t few_n;
+  uint64_t few[kFew];                 // this CTA's keys of the bin: key, then the lower slot first
+  uint32_t cut;
+  int32_t cut_slot;
+  int32_t list[2 * kSmemList];
 };
 
-__global__ void __launch_bounds__(kThreads) kv_evict_kernel(KvEvictArgs a) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant__ KvEvictArgs a) {
+  constexpr int WARPS = THREADS / 32;
   extern __shared__ uint32_t s_keys[];
-  __shared__ Shared s;
+  __shared__ Shared<WARPS> s;
   cg::cluster_group cluster = cg::this_cluster();
-  const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int cs = (int)cluster.num_blocks(), rank = cs == 1 ? 0 : (int)cluster.block_rank();
+  auto sync = [&]() {
+    if (cs == 1) __syncthreads();
+    else cluster.sync();
+  };
+  // a value of CTA r of the cluster
+  auto of = [&](auto* p, int r) { return cs == 1 ? *p : *cluster.map_shared_rank(p, r); };
   const int64_t unit = blockIdx.x / cs;
   const int b = (int)(unit / a.n_kv_heads), h = (int)(unit - (int64_t)b * a.n_kv_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t base = unit * a.slots;      // of weights and slot_pos
+  const int32_t newest = __ldg(a.pos + b);
   const int32_t n = kv_clamp_len(__ldg(a.lens + b), a.max_len, b, a.err);
   const int32_t budget = a.budget;
   const int32_t left = n < budget ? n : budget;
@@ -67,15 +87,16 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(KvEvictArgs a) {
 
   if (h == 0 && rank == 0 && tid == 0 && a.lens_out != a.lens) a.lens_out[b] = left;
   // beyond the old length both arrays are zero
-  for (int64_t j = n + rank * kThreads + tid; j < a.max_len; j += (int64_t)cs * kThreads) {
+  for (int64_t j = n + rank * THREADS + tid; j < a.max_len; j += (int64_t)cs * THREADS) {
     a.weights_out[base + j] = 0.f;
     a.slot_pos_out[base + j] = 0;
   }
   if (a.src_out)
-    for (int64_t j = left + rank * kThreads + tid; j < budget; j += (int64_t)cs * kThreads)
+    for (int64_t j = left + rank * THREADS + tid; j < budget; j += (int64_t)cs * THREADS)
       a.src_out[unit * budget + j] = -1;
   if (n <= budget) {   // nothing leaves (the whole cluster takes this branch)
-    for (int j = rank * kThreads + tid; j < n; j += cs * kThreads) {
+#pragma unroll 4
+    for (int j = rank * THREADS + tid; j < n; j += cs * THREADS) {
       if (!inplace) a.weights_out[base + j] = a.weights[base + j];
       if (!pos_inplace) a.slot_pos_out[base + j] = a.slot_pos[base + j];
       if (a.src_out) a.src_out[unit * budget + j] = j;
@@ -83,51 +104,60 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(KvEvictArgs a) {
     return;
   }
 
-  const int32_t newest = __ldg(a.pos + b);
   // runs of whole 32-slot rows, one per warp of the cluster
-  const int32_t run = (int32_t)((((int64_t)n + cs * kWarps - 1) / (cs * kWarps) + 31) / 32 * 32);
-  const int64_t cta0 = (int64_t)rank * kWarps * run;
+  const int32_t run = (int32_t)((((int64_t)n + cs * WARPS - 1) / (cs * WARPS) + 31) / 32 * 32);
+  const int64_t cta0 = (int64_t)rank * WARPS * run;
   const int64_t w0 = cta0 + (int64_t)warp * run;
   const int32_t w_end = (int32_t)(w0 + run < n ? w0 + run : n);
-  const bool cached = (int64_t)run * kWarps <= a.key_cap;
+  const bool cached = (int64_t)run * WARPS <= a.key_cap;
 
-  for (int i = tid; i < 4 * 256; i += kThreads) (&s.hist[0][0])[i] = 0;
+  for (int i = tid; i < 4 * 256; i += THREADS) (&s.hist[0][0])[i] = 0;
+  if (tid == 0) s.few_n = 0;
   __syncthreads();
 
   auto key_at = [&](int32_t j) -> uint32_t {
     return cached ? s_keys[j - cta0] : slot_key(a, base + j, newest);
   };
 
-  // ---- the budget-th largest key -------------------------------------------
-  uint32_t prefix = 0;
-  uint32_t need = (uint32_t)budget, equal = 0;
+  // ---- the budget-th largest (key, lower slot first) ---------------------------
+  uint32_t prefix = 0, need = (uint32_t)budget, cut = 0;
+  int32_t cut_slot = 0x7fffffff;   // slots on the cut stay up to this one
+  int last_shift = 0;
+  bool few = false, ties = false;
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
-    for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
-      uint32_t key;
-      if (pass == 0) {
-        key = slot_key(a, base + j, newest);
+    if (pass == 0) {
+      uint32_t held = 0;   // one shared address for all of them: counted per thread
+#pragma unroll 4
+      for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
+        const uint32_t key = slot_key(a, base + j, newest);
         if (cached) s_keys[j - cta0] = key;
-      } else {
-        key = key_at(j);
+        if (key == kHeld) ++held;
+        else atomicAdd(&s.hist[0][key >> 24], 1u);
       }
-      if (pass == 0 || (key >> (shift + 8)) == prefix) atomicAdd(&s.hist[pass][(key >> shift) & 255u], 1u);
+      held = __reduce_add_sync(0xffffffffu, held);
+      if (lane == 0 && held) atomicAdd(&s.hist[0][255], held);
+    } else {
+      for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
+        const uint32_t key = key_at(j);
+        if ((key >> (shift + 8)) == prefix) atomicAdd(&s.hist[pass][(key >> shift) & 255u], 1u);
+      }
     }
-    cluster.sync();
-    if (warp < 8) {   // 8 warps, one bin per thread, bins in descending order
+    sync();
+    if (warp < 8) {   // one bin per thread, bins in descending order
       const int bin = 255 - tid;
       uint32_t c = 0;
-      for (int r = 0; r < cs; ++r) c += *cluster.map_shared_rank(&s.hist[pass][bin], r);
+      for (int r = 0; r < cs; ++r) c += of(&s.hist[pass][bin], r);
       uint32_t up = c;   // keys in this bin and the higher ones of the warp
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t v = __shfl_up_sync(0xffffffffu, up, o);
         if (lane >= o) up += v;
       }
-      if (lane == 31) s.warp_eq[warp] = (int32_t)up;
+      if (lane == 31) s.warp_a[warp] = (int32_t)up;
       named_barrier_sync(1, 256);
-      for (int w = 0; w < warp; ++w) up += (uint32_t)s.warp_eq[w];
+      for (int w = 0; w < warp; ++w) up += (uint32_t)s.warp_a[w];
       if (up >= need && up - c < need) {
         s.bin = (uint32_t)bin;
         s.above = up - c;
@@ -137,104 +167,145 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(KvEvictArgs a) {
     __syncthreads();
     prefix = (prefix << 8) | s.bin;
     need -= s.above;
-    equal = s.count;
-  }
-  const uint32_t cut = prefix;   // keys above it stay, and the `need` lowest slots of the `equal` on it
-
-  // ---- ranks of the equal keys ---------------------------------------------
-  int32_t eq_before = 0;
-  if (need < equal) {
-    int32_t c = 0;
-    for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
-      const int32_t j = j0 + lane;
-      c += __popc(__ballot_sync(0xffffffffu, j < w_end && key_at(j) == cut));
+    const uint32_t count = s.count;
+    cut = prefix << shift;
+    last_shift = shift;
+    if (need == count) break;          // the whole bin stays
+    if (count <= kFew) {
+      few = true;
+      break;
     }
-    if (lane == 0) s.warp_eq[warp] = c;
+    ties = pass == 3;
+  }
+  if (few) {   // rank the bin's keys; every CTA looks at all of the cluster's
+    for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
+      const uint32_t key = key_at(j);
+      if ((key >> last_shift) == prefix) s.few[atomicAdd(&s.few_n, 1u)] = (uint64_t)key << 32 | (uint32_t)~j;
+    }
+    sync();
+    if (warp < kFew / 32) {
+      uint64_t mine = 0;
+      int at = tid;
+      for (int r = 0; r < cs; ++r) {
+        const int m = (int)of(&s.few_n, r);
+        if (at >= 0 && at < m) mine = of(&s.few[at], r);
+        at -= m;
+      }
+      uint32_t above = 0;
+      for (int r = 0; r < cs; ++r)
+        for (int k = 0, m = (int)of(&s.few_n, r); k < m; ++k) above += of(&s.few[k], r) > mine;
+      if (mine != 0 && above == need - 1) {
+        s.cut = (uint32_t)(mine >> 32);
+        s.cut_slot = (int32_t)~(uint32_t)mine;
+      }
+    }
+    __syncthreads();
+    cut = s.cut;
+    cut_slot = s.cut_slot;
+  }
+  if (ties) {   // the need-th lowest slot of those on the cut
+    int32_t c = 0;
+    for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32)
+      c += __popc(__ballot_sync(0xffffffffu, j0 + lane < w_end && key_at(j0 + lane) == cut));
+    if (lane == 0) s.warp_a[warp] = c;
     __syncthreads();
     if (tid == 0) {
-      int32_t t = 0;
-      for (int w = 0; w < kWarps; ++w) t += s.warp_eq[w];
-      s.cta_eq = t;
+      int32_t sum = 0;
+      for (int w = 0; w < WARPS; ++w) sum += s.warp_a[w];
+      s.cta_a = sum;
     }
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) eq_before += *cluster.map_shared_rank(&s.cta_eq, r);
-    for (int w = 0; w < warp; ++w) eq_before += s.warp_eq[w];
-  }
-  // Calls f(j, stays) for the warp's slots, a 32-slot row at a time (j >= w_end: none).
-  auto walk = [&](auto f) {
-    int32_t rank_eq = eq_before;
-    for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
-      const int32_t j = j0 + lane;
-      const uint32_t key = j < w_end ? key_at(j) : 0u;
-      const bool eq = j < w_end && key == cut;
-      bool stays = j < w_end && key > cut;
-      if (need < equal) {
+    sync();
+    int32_t before = 0;
+    for (int r = 0; r < rank; ++r) before += of(&s.cta_a, r);
+    for (int w = 0; w < warp; ++w) before += s.warp_a[w];
+    if (before < (int32_t)need && before + c >= (int32_t)need) {   // in this warp's run
+      for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
+        const bool eq = j0 + lane < w_end && key_at(j0 + lane) == cut;
         const uint32_t m = __ballot_sync(0xffffffffu, eq);
-        stays |= eq && (uint32_t)(rank_eq + __popc(m & ((1u << lane) - 1u))) < need;
-        rank_eq += __popc(m);
-      } else {
-        stays |= eq;
+        if (eq && before + __popc(m & ((2u << lane) - 1u)) == (int32_t)need) {
+          if (cs == 1) s.cut_slot = j0 + lane;
+          else
+            for (int r = 0; r < cs; ++r) *cluster.map_shared_rank(&s.cut_slot, r) = j0 + lane;
+        }
+        before += __popc(m);
       }
-      f(j, stays);
     }
-  };
+    sync();
+    cut_slot = s.cut_slot;
+  }
+
   // ---- number the holes and the movers -------------------------------------
+  auto stays = [&](int32_t j) {
+    const uint32_t key = key_at(j);
+    return key > cut || (key == cut && j <= cut_slot);
+  };
   int32_t holes = 0, moves = 0;
-  walk([&](int32_t j, bool stays) {
-    holes += __popc(__ballot_sync(0xffffffffu, j < w_end && j < budget && !stays));
-    moves += __popc(__ballot_sync(0xffffffffu, j >= budget && stays));
-  });
+  for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
+    const int32_t j = j0 + lane;
+    const bool in = j < w_end, st = in && stays(j);
+    holes += __popc(__ballot_sync(0xffffffffu, in && j < budget && !st));
+    moves += __popc(__ballot_sync(0xffffffffu, j >= budget && st));
+  }
+  __syncthreads();   // warp_a may still be read
   if (lane == 0) {
-    s.warp_hole[warp] = holes;
-    s.warp_move[warp] = moves;
+    s.warp_a[warp] = holes;
+    s.warp_b[warp] = moves;
   }
   __syncthreads();
-  if (tid == 0) {
-    int32_t x = 0, y = 0;
-    for (int w = 0; w < kWarps; ++w) x += s.warp_hole[w], y += s.warp_move[w];
-    s.cta_hole = x;
-    s.cta_move = y;
-  }
-  cluster.sync();
   int32_t hole_at = 0, move_at = 0, total = 0;
-  for (int r = 0; r < cs; ++r) {
-    const int32_t x = *cluster.map_shared_rank(&s.cta_hole, r);
-    if (r < rank) {
-      hole_at += x;
-      move_at += *cluster.map_shared_rank(&s.cta_move, r);
+  if (cs > 1) {
+    if (tid == 0) {
+      int32_t x = 0, y = 0;
+      for (int w = 0; w < WARPS; ++w) x += s.warp_a[w], y += s.warp_b[w];
+      s.cta_b = x;
+      s.count = (uint32_t)y;
     }
-    total += x;   // as many holes as movers: exactly `budget` slots stay
+    cluster.sync();
+    for (int r = 0; r < cs; ++r) {
+      const int32_t x = of(&s.cta_b, r);
+      if (r < rank) {
+        hole_at += x;
+        move_at += (int32_t)of(&s.count, r);
+      }
+      total += x;   // as many holes as movers: exactly `budget` slots stay
+    }
   }
-  for (int w = 0; w < warp; ++w) hole_at += s.warp_hole[w], move_at += s.warp_move[w];
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) hole_at += s.warp_a[w], move_at += s.warp_b[w];
+    if (cs == 1) total += s.warp_a[w];
+  }
 
   // ---- list them; the slots that keep or lose what they hold ----------------
-  int32_t* const to = a.list + unit * 2 * a.list_len;
-  int32_t* const from = to + a.list_len;
-  walk([&](int32_t j, bool stays) {
+  const bool near = cs == 1 && total <= kSmemList;
+  int32_t* const to = near ? s.list : a.list + unit * 2 * a.list_len;
+  int32_t* const from = near ? s.list + kSmemList : to + a.list_len;
+  for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
+    const int32_t j = j0 + lane;
     const uint32_t below = (1u << lane) - 1u;
-    const bool hole = j < w_end && j < budget && !stays, mover = j >= budget && stays;
+    const bool in = j < w_end, low = in && j < budget, st = in && stays(j);
+    const bool hole = low && !st, mover = st && j >= budget;
     const uint32_t mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
     if (hole) to[hole_at + __popc(mh & below)] = j;
     if (mover) from[move_at + __popc(mm & below)] = j;
     hole_at += __popc(mh);
     move_at += __popc(mm);
-    if (j < w_end && j < budget && stays) {
+    if (low && st) {
       if (!inplace) a.weights_out[base + j] = a.weights[base + j];
       if (!pos_inplace) a.slot_pos_out[base + j] = a.slot_pos[base + j];
       if (a.src_out) a.src_out[unit * budget + j] = j;
     }
-    if (j < w_end && j >= budget) {   // in place a mover's are cleared once they have been read
+    if (in && j >= budget) {   // in place a mover's are cleared once they have been read
       if (!inplace || !mover) a.weights_out[base + j] = 0.f;
       if (!pos_inplace || !mover) a.slot_pos_out[base + j] = 0;
     }
-  });
-  cluster.sync();   // the lists are complete (and no CTA leaves while its counts are read)
+  }
+  sync();   // the lists are complete (and no CTA leaves while its counts are read)
 
   // ---- move rows -------------------------------------------------------------
   const uint32_t per_row = a.shared ? a.chunks : 2 * a.chunks;   // 16-byte pieces of a key and a value
   const uint32_t items = (uint32_t)total * per_row;   // budget <= 2^24: below 2^30
-  const uint32_t step = cs * kThreads;
-  for (uint32_t i0 = rank * kThreads + tid; i0 < items; i0 += step * kUnroll) {
+  const uint32_t step = cs * THREADS;
+  for (uint32_t i0 = rank * THREADS + tid; i0 < items; i0 += step * kUnroll) {
     uint4 val[kUnroll];
     char* dst[kUnroll];
 #pragma unroll
@@ -282,33 +353,44 @@ __global__ void __launch_bounds__(256) kv_evict_lengths_kernel(KvEvictArgs a) {
 
 }  // namespace
 
-cudaError_t launch_kv_evict(const Launch& L, const KvEvictArgs& args) {
-  KvEvictArgs a = args;
+template <int THREADS>
+static cudaError_t launch_threads(const Launch& L, KvEvictArgs& a, int cs) {
   const int64_t units = (int64_t)a.B * a.n_kv_heads;
-  int cs = 1;
-  while (cs < kMaxCluster && a.max_len > 512 * cs && (a.max_len > 4096 * cs || units * cs * 2 <= 148)) cs *= 2;
-  const int64_t run = ((a.max_len + cs * kWarps - 1) / (cs * kWarps) + 31) / 32 * 32;
-  a.key_cap = (int32_t)(run * kWarps <= kMaxCachedKeys ? run * kWarps : kMaxCachedKeys);
-  const size_t smem = (size_t)a.key_cap * sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const int per = cs * THREADS;   // slots a run advances by
+  const int64_t run = ((a.max_len + per / 32 - 1) / (per / 32) + 31) / 32 * 32 * (THREADS / 32);
+  a.key_cap = (int32_t)(run <= kMaxCachedKeys ? run : kMaxCachedKeys);
+  cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kMaxCachedKeys * (int)sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cs));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = (size_t)a.key_cap * sizeof(uint32_t);
   cfg.stream = L.stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)cs;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
   L.begin(kKernelKvEvict);
-  e = cudaLaunchKernelEx(&cfg, kv_evict_kernel, a);
+  e = cudaLaunchKernelEx(&cfg, kv_evict_kernel<THREADS>, a);
   if (e != cudaSuccess) return e;
-  e = L.end(kKernelKvEvict);
+  return L.end(kKernelKvEvict);
+}
+
+// CTAs per (sequence, head) and their threads: enough for four CTAs of 256
+// threads on every SM, as long as a CTA keeps 512 slots; where even eight a head
+// leave SMs idle, CTAs of 1024 threads.
+cudaError_t launch_kv_evict(const Launch& L, const KvEvictArgs& args) {
+  KvEvictArgs a = args;
+  const int64_t units = (int64_t)a.B * a.n_kv_heads;
+  int cs = 1;
+  while (cs < kMaxCluster && a.max_len > 512 * cs && (units * cs * 2 <= 4 * 148 || a.max_len > (int64_t)kMaxCachedKeys * cs)) cs *= 2;
+  const bool wide = units * cs <= 148 && a.max_len > 1024 * cs;
+  cudaError_t e = wide ? launch_threads<1024>(L, a, cs) : launch_threads<256>(L, a, cs);
   if (e != cudaSuccess || a.lens_out != a.lens) return e;
+  L.begin(kKernelKvEvict);
   kv_evict_lengths_kernel<<<(unsigned)((a.B + 255) / 256), 256, 0, L.stream>>>(a);
   return L.end(kKernelKvEvict);
 }
