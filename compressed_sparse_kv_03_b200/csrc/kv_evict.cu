@@ -15,11 +15,12 @@
 //   2. radix select, 8 bits a pass: a histogram per CTA, summed over the
 //      cluster through distributed shared memory, until the bin that holds the
 //      budget-th key is wholly kept, or holds at most 64 keys, which are ranked
-//      directly by (key, slot); only keys with more than 64 equals go through
-//      all four passes and are then ranked by slot;
+//      directly by (key, slot); where more than 64 equal keys (slots that were
+//      never looked at) straddle the budget, they are ranked by slot;
 //   3. the staying slots above the budget and the holes below it are numbered
 //      in order and listed;
-//   4. all CTAs of the cluster copy the listed rows, 16 bytes a thread.
+//   4. a thread per listed row looks its pages up and moves its weight and
+//      position; then all CTAs of the cluster copy the rows, 16 bytes a thread.
 // Sources lie at or above the budget and targets below it, so the copies need
 // no order.  Bound by latency (a chain of about five loads and ten barriers)
 // until some hundred rows move, then by HBM.
@@ -37,14 +38,13 @@ namespace {
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCachedKeys = 24576;   // 96 KB of keys per CTA
 constexpr int kUnroll = 4;              // row pieces in flight per thread
+constexpr int kLoads = 4;               // weights and positions in flight per thread
 constexpr int kFew = 64;                // keys of a bin that are ranked directly
 constexpr int kSmemList = 512;          // moves listed in shared memory (clusters of one)
 constexpr uint32_t kHeld = 0xffffffffu;
 
-__device__ __forceinline__ uint32_t slot_key(const KvEvictArgs& a, int64_t at, int32_t newest) {
-  const int32_t p = a.slot_pos[at];
+__device__ __forceinline__ uint32_t slot_key(const KvEvictArgs& a, float w, int32_t p, int32_t newest) {
   if ((int64_t)p > (int64_t)newest - a.recent || p < a.keep_first) return kHeld;
-  const float w = a.weights[at];
   return w != w ? kHeld - 1 : score_key(w);   // +inf is below kHeld - 1
 }
 
@@ -56,9 +56,12 @@ struct Shared {
   uint32_t bin, above, count;
   uint32_t few_n;
   uint64_t few[kFew];                 // this CTA's keys of the bin: key, then the lower slot first
+  uint64_t all_few[kFew];             // the cluster's
+  uint32_t key_and[4], key_or[4];     // of a pass's candidates
   uint32_t cut;
   int32_t cut_slot;
   int32_t list[2 * kSmemList];
+  int4 pages[kSmemList];
 };
 
 template <int THREADS>
@@ -112,11 +115,15 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
   const bool cached = (int64_t)run * WARPS <= a.key_cap;
 
   for (int i = tid; i < 4 * 256; i += THREADS) (&s.hist[0][0])[i] = 0;
+  if (tid < 4) {
+    s.key_and[tid] = 0xffffffffu;
+    s.key_or[tid] = 0u;
+  }
   if (tid == 0) s.few_n = 0;
   __syncthreads();
 
   auto key_at = [&](int32_t j) -> uint32_t {
-    return cached ? s_keys[j - cta0] : slot_key(a, base + j, newest);
+    return cached ? s_keys[j - cta0] : slot_key(a, a.weights[base + j], a.slot_pos[base + j], newest);
   };
 
   // ---- the budget-th largest (key, lower slot first) ---------------------------
@@ -129,26 +136,57 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
     const int shift = 24 - 8 * pass;
     if (pass == 0) {
       uint32_t held = 0;   // one shared address for all of them: counted per thread
-#pragma unroll 4
-      for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
-        const uint32_t key = slot_key(a, base + j, newest);
-        if (cached) s_keys[j - cta0] = key;
-        if (key == kHeld) ++held;
-        else atomicAdd(&s.hist[0][key >> 24], 1u);
+      for (int32_t j0 = (int32_t)w0 + lane; j0 < w_end; j0 += 32 * kLoads) {
+        float w[kLoads];
+        int32_t sp[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int32_t j = j0 + 32 * u;
+          w[u] = j < w_end ? a.weights[base + j] : 0.f;
+          sp[u] = j < w_end ? a.slot_pos[base + j] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const int32_t j = j0 + 32 * u;
+          if (j >= w_end) break;
+          const uint32_t key = slot_key(a, w[u], sp[u], newest);
+          if (cached) s_keys[j - cta0] = key;
+          if (key == kHeld) ++held;
+          else atomicAdd(&s.hist[0][key >> 24], 1u);
+          // as if every slot below the budget stayed: the holes are overwritten
+          if (!inplace) a.weights_out[base + j] = j < budget ? w[u] : 0.f;
+          if (!pos_inplace) a.slot_pos_out[base + j] = j < budget ? sp[u] : 0;
+          if (a.src_out && j < budget) a.src_out[unit * budget + j] = j;
+        }
       }
       held = __reduce_add_sync(0xffffffffu, held);
       if (lane == 0 && held) atomicAdd(&s.hist[0][255], held);
     } else {
+      uint32_t all_and = 0xffffffffu, all_or = 0u;
       for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
         const uint32_t key = key_at(j);
-        if ((key >> (shift + 8)) == prefix) atomicAdd(&s.hist[pass][(key >> shift) & 255u], 1u);
+        if ((key >> (shift + 8)) != prefix) continue;
+        atomicAdd(&s.hist[pass][(key >> shift) & 255u], 1u);
+        all_and &= key;
+        all_or |= key;
+      }
+      all_and = __reduce_and_sync(0xffffffffu, all_and);
+      all_or = __reduce_or_sync(0xffffffffu, all_or);
+      if (lane == 0 && all_or != 0u) {
+        atomicAnd(&s.key_and[pass], all_and);
+        atomicOr(&s.key_or[pass], all_or);
       }
     }
     sync();
     if (warp < 8) {   // one bin per thread, bins in descending order
       const int bin = 255 - tid;
       uint32_t c = 0;
-      for (int r = 0; r < cs; ++r) c += of(&s.hist[pass][bin], r);
+      if (cs == 1) {
+        c = s.hist[pass][bin];
+      } else {
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) c += r < cs ? of(&s.hist[pass][bin], r) : 0u;
+      }
       uint32_t up = c;   // keys in this bin and the higher ones of the warp
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -175,7 +213,16 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
       few = true;
       break;
     }
-    ties = pass == 3;
+    if (pass > 0) {
+      uint32_t all_and = s.key_and[pass], all_or = s.key_or[pass];
+      for (int r = 0; cs > 1 && r < cs; ++r) all_and &= of(&s.key_and[pass], r), all_or |= of(&s.key_or[pass], r);
+      if (all_and == all_or) {         // all candidates are one key
+        cut = all_and;
+        ties = true;
+        break;
+      }
+    }
+    ties = pass == 3;                  // all of the bin's are
   }
   if (few) {   // rank the bin's keys; every CTA looks at all of the cluster's
     for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
@@ -191,9 +238,11 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
         if (at >= 0 && at < m) mine = of(&s.few[at], r);
         at -= m;
       }
+      s.all_few[tid] = mine;
+      named_barrier_sync(1, kFew);
       uint32_t above = 0;
-      for (int r = 0; r < cs; ++r)
-        for (int k = 0, m = (int)of(&s.few_n, r); k < m; ++k) above += of(&s.few[k], r) > mine;
+#pragma unroll 16
+      for (int k = 0; k < kFew; ++k) above += s.all_few[k] > mine;
       if (mine != 0 && above == need - 1) {
         s.cut = (uint32_t)(mine >> 32);
         s.cut_slot = (int32_t)~(uint32_t)mine;
@@ -261,11 +310,12 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
       s.count = (uint32_t)y;
     }
     cluster.sync();
-    for (int r = 0; r < cs; ++r) {
-      const int32_t x = of(&s.cta_b, r);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      const int32_t x = r < cs ? of(&s.cta_b, r) : 0, y = r < cs ? (int32_t)of(&s.count, r) : 0;
       if (r < rank) {
         hole_at += x;
-        move_at += (int32_t)of(&s.count, r);
+        move_at += y;
       }
       total += x;   // as many holes as movers: exactly `budget` slots stay
     }
@@ -275,67 +325,64 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
     if (cs == 1) total += s.warp_a[w];
   }
 
-  // ---- list them; the slots that keep or lose what they hold ----------------
+  // ---- list them ---------------------------------------------------------------
   const bool near = cs == 1 && total <= kSmemList;
+  int4* const pages = near ? s.pages : a.pages + unit * a.list_len;   // (from page, row, to page, row); from page -1: not copied
   int32_t* const to = near ? s.list : a.list + unit * 2 * a.list_len;
   int32_t* const from = near ? s.list + kSmemList : to + a.list_len;
   for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
     const int32_t j = j0 + lane;
     const uint32_t below = (1u << lane) - 1u;
-    const bool in = j < w_end, low = in && j < budget, st = in && stays(j);
-    const bool hole = low && !st, mover = st && j >= budget;
+    const bool in = j < w_end, st = in && stays(j);
+    const bool hole = in && j < budget && !st, mover = st && j >= budget;
     const uint32_t mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
     if (hole) to[hole_at + __popc(mh & below)] = j;
     if (mover) from[move_at + __popc(mm & below)] = j;
     hole_at += __popc(mh);
     move_at += __popc(mm);
-    if (low && st) {
-      if (!inplace) a.weights_out[base + j] = a.weights[base + j];
-      if (!pos_inplace) a.slot_pos_out[base + j] = a.slot_pos[base + j];
-      if (a.src_out) a.src_out[unit * budget + j] = j;
-    }
-    if (in && j >= budget) {   // in place a mover's are cleared once they have been read
-      if (!inplace || !mover) a.weights_out[base + j] = 0.f;
-      if (!pos_inplace || !mover) a.slot_pos_out[base + j] = 0;
+    if (in && j >= budget && !mover) {   // in place a mover's are cleared once they have been read
+      if (inplace) a.weights_out[base + j] = 0.f;
+      if (pos_inplace) a.slot_pos_out[base + j] = 0;
     }
   }
   sync();   // the lists are complete (and no CTA leaves while its counts are read)
 
   // ---- move rows -------------------------------------------------------------
+  // A CTA looks up what it copies itself: pairs rank, rank + cs, ..
+  const int mine = (total - rank + cs - 1) / cs;
+  for (int i = tid; i < mine; i += THREADS) {
+    const int pair = i * cs + rank;
+    const int32_t d_slot = to[pair], s_slot = from[pair];
+    a.weights_out[base + d_slot] = a.weights[base + s_slot];
+    a.slot_pos_out[base + d_slot] = a.slot_pos[base + s_slot];
+    if (inplace) a.weights_out[base + s_slot] = 0.f;
+    if (pos_inplace) a.slot_pos_out[base + s_slot] = 0;
+    if (a.src_out) a.src_out[unit * budget + d_slot] = s_slot;
+    int4 pg;
+    pg.x = kv_page(a.kv, b, s_slot, &pg.y, a.err);
+    pg.z = kv_page(a.kv, b, d_slot, &pg.w, a.err);
+    if (pg.z < 0) pg.x = -1;
+    pages[pair] = pg;
+  }
+  __syncthreads();
   const uint32_t per_row = a.shared ? a.chunks : 2 * a.chunks;   // 16-byte pieces of a key and a value
-  const uint32_t items = (uint32_t)total * per_row;   // budget <= 2^24: below 2^30
-  const uint32_t step = cs * THREADS;
-  for (uint32_t i0 = rank * THREADS + tid; i0 < items; i0 += step * kUnroll) {
+  const uint32_t items = (uint32_t)mine * per_row;   // budget <= 2^24: below 2^30
+  for (uint32_t i0 = tid; i0 < items; i0 += THREADS * kUnroll) {
     uint4 val[kUnroll];
     char* dst[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t i = i0 + u * step;
-      dst[u] = nullptr;
-      if (i >= items) continue;
-      const uint32_t pair = i / per_row;
-      const int p = (int)(i - pair * per_row);
-      const int32_t d_slot = to[pair], s_slot = from[pair];
-      if (p == 0) {
-        a.weights_out[base + d_slot] = a.weights[base + s_slot];
-        a.slot_pos_out[base + d_slot] = a.slot_pos[base + s_slot];
-        if (inplace) a.weights_out[base + s_slot] = 0.f;
-        if (pos_inplace) a.slot_pos_out[base + s_slot] = 0;
-        if (a.src_out) a.src_out[unit * budget + d_slot] = s_slot;
-      }
-      int32_t d_row, s_row;
-      const int32_t d_page = kv_page(a.kv, b, d_slot, &d_row, a.err);
-      const int32_t s_page = kv_page(a.kv, b, s_slot, &s_row, a.err);
-      if (d_page < 0 || s_page < 0) continue;
-      if (p < a.chunks) {
-        const int64_t off = h * a.kv.k_head + 16 * p;
-        val[u] = *reinterpret_cast<const uint4*>(a.kv.k + s_page * a.kv.k_page + s_row * a.kv.k_slot + off);
-        dst[u] = a.kv.k + d_page * a.kv.k_page + d_row * a.kv.k_slot + off;
-      } else {
-        const int64_t off = h * a.kv.v_head + 16 * (p - a.chunks);
-        val[u] = *reinterpret_cast<const uint4*>(a.kv.v + s_page * a.kv.v_page + s_row * a.kv.v_slot + off);
-        dst[u] = a.kv.v + d_page * a.kv.v_page + d_row * a.kv.v_slot + off;
-      }
+      const uint32_t i = i0 + u * THREADS;
+      const uint32_t row = i / per_row;
+      const bool in = i < items;
+      const int4 pg = in ? pages[row * cs + rank] : make_int4(-1, 0, 0, 0);
+      const int p = (int)(i - row * per_row);
+      const bool is_v = p >= a.chunks;
+      const int64_t off = is_v ? h * a.kv.v_head + 16 * (p - a.chunks) : h * a.kv.k_head + 16 * p;
+      const int64_t page_st = is_v ? a.kv.v_page : a.kv.k_page, slot_st = is_v ? a.kv.v_slot : a.kv.k_slot;
+      char* const data = (is_v ? a.kv.v : a.kv.k) + off;
+      dst[u] = pg.x >= 0 ? data + pg.z * page_st + pg.w * slot_st : nullptr;
+      if (pg.x >= 0) val[u] = *reinterpret_cast<const uint4*>(data + pg.x * page_st + pg.y * slot_st);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
