@@ -38,7 +38,7 @@ namespace {
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCachedKeys = 24576;   // 96 KB of keys per CTA
 constexpr int kUnroll = 4;              // row pieces in flight per thread
-constexpr int kLoads = 4;               // weights and positions in flight per thread
+constexpr int kLoads = 9;               // weights and positions in flight per thread
 constexpr int kFew = 64;                // keys of a bin that are ranked directly
 constexpr int kSmemList = 512;          // moves listed in shared memory (clusters of one)
 constexpr uint32_t kHeld = 0xffffffffu;
@@ -55,8 +55,8 @@ struct Shared {
   int32_t cta_a, cta_b;
   uint32_t bin, above, count;
   uint32_t few_n;
-  uint64_t few[kFew];                 // this CTA's keys of the bin: key, then the lower slot first
-  uint64_t all_few[kFew];             // the cluster's
+  uint64_t few[kFew];                 // the cluster's keys of the bin: key, then the lower slot first
+  uint64_t least[WARPS];
   uint32_t key_and[4], key_or[4];     // of a pass's candidates
   uint32_t cut;
   int32_t cut_slot;
@@ -65,7 +65,7 @@ struct Shared {
 };
 
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant__ KvEvictArgs a) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const __grid_constant__ KvEvictArgs a) {
   constexpr int WARPS = THREADS / 32;
   extern __shared__ uint32_t s_keys[];
   __shared__ Shared<WARPS> s;
@@ -126,6 +126,11 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
     return cached ? s_keys[j - cta0] : slot_key(a, a.weights[base + j], a.slot_pos[base + j], newest);
   };
 
+  // One slot too many (a step at the budget): no threshold is needed, only the
+  // least (key, higher slot first).
+  const bool one = n - budget == 1;
+  uint64_t least = ~0ull;
+
   // ---- the budget-th largest (key, lower slot first) ---------------------------
   uint32_t prefix = 0, need = (uint32_t)budget, cut = 0;
   int32_t cut_slot = 0x7fffffff;   // slots on the cut stay up to this one
@@ -151,18 +156,26 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
           if (j >= w_end) break;
           const uint32_t key = slot_key(a, w[u], sp[u], newest);
           if (cached) s_keys[j - cta0] = key;
-          if (key == kHeld) ++held;
-          else atomicAdd(&s.hist[0][key >> 24], 1u);
+          if (one) {
+            const uint64_t x = (uint64_t)key << 32 | (uint32_t)~j;
+            least = x < least ? x : least;
+          } else if (key == kHeld) {
+            ++held;
+          } else {
+            atomicAdd(&s.hist[0][key >> 24], 1u);
+          }
           // as if every slot below the budget stayed: the holes are overwritten
           if (!inplace) a.weights_out[base + j] = j < budget ? w[u] : 0.f;
           if (!pos_inplace) a.slot_pos_out[base + j] = j < budget ? sp[u] : 0;
           if (a.src_out && j < budget) a.src_out[unit * budget + j] = j;
         }
       }
+      if (one) break;
       held = __reduce_add_sync(0xffffffffu, held);
       if (lane == 0 && held) atomicAdd(&s.hist[0][255], held);
     } else {
       uint32_t all_and = 0xffffffffu, all_or = 0u;
+#pragma unroll 4
       for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
         const uint32_t key = key_at(j);
         if ((key >> (shift + 8)) != prefix) continue;
@@ -224,26 +237,26 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
     }
     ties = pass == 3;                  // all of the bin's are
   }
-  if (few) {   // rank the bin's keys; every CTA looks at all of the cluster's
+  if (few) {   // rank the bin's keys: they gather in every CTA, in any order
     for (int32_t j = (int32_t)w0 + lane; j < w_end; j += 32) {
       const uint32_t key = key_at(j);
-      if ((key >> last_shift) == prefix) s.few[atomicAdd(&s.few_n, 1u)] = (uint64_t)key << 32 | (uint32_t)~j;
+      if ((key >> last_shift) != prefix) continue;
+      const uint64_t x = (uint64_t)key << 32 | (uint32_t)~j;
+      if (cs == 1) {
+        s.few[atomicAdd(&s.few_n, 1u)] = x;
+      } else {
+        const uint32_t at = atomicAdd(cluster.map_shared_rank(&s.few_n, 0), 1u);
+        for (int r = 0; r < cs; ++r) *cluster.map_shared_rank(&s.few[at], r) = x;
+      }
     }
     sync();
     if (warp < kFew / 32) {
-      uint64_t mine = 0;
-      int at = tid;
-      for (int r = 0; r < cs; ++r) {
-        const int m = (int)of(&s.few_n, r);
-        if (at >= 0 && at < m) mine = of(&s.few[at], r);
-        at -= m;
-      }
-      s.all_few[tid] = mine;
-      named_barrier_sync(1, kFew);
+      const int m = (int)s.count;
+      const uint64_t mine = tid < m ? s.few[tid] : 0;
       uint32_t above = 0;
 #pragma unroll 16
-      for (int k = 0; k < kFew; ++k) above += s.all_few[k] > mine;
-      if (mine != 0 && above == need - 1) {
+      for (int k = 0; k < kFew; ++k) above += k < m && s.few[k] > mine;
+      if (tid < m && above == need - 1) {
         s.cut = (uint32_t)(mine >> 32);
         s.cut_slot = (int32_t)~(uint32_t)mine;
       }
@@ -258,15 +271,14 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
       c += __popc(__ballot_sync(0xffffffffu, j0 + lane < w_end && key_at(j0 + lane) == cut));
     if (lane == 0) s.warp_a[warp] = c;
     __syncthreads();
-    if (tid == 0) {
-      int32_t sum = 0;
-      for (int w = 0; w < WARPS; ++w) sum += s.warp_a[w];
-      s.cta_a = sum;
+    const int32_t x = lane < WARPS ? s.warp_a[lane] : 0;
+    int32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
+    if (cs > 1) {
+      const int32_t sum = __reduce_add_sync(0xffffffffu, x);
+      if (tid == 0) s.cta_a = sum;
+      cluster.sync();
+      before += __reduce_add_sync(0xffffffffu, lane < rank ? *cluster.map_shared_rank(&s.cta_a, lane) : 0);
     }
-    sync();
-    int32_t before = 0;
-    for (int r = 0; r < rank; ++r) before += of(&s.cta_a, r);
-    for (int w = 0; w < warp; ++w) before += s.warp_a[w];
     if (before < (int32_t)need && before + c >= (int32_t)need) {   // in this warp's run
       for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
         const bool eq = j0 + lane < w_end && key_at(j0 + lane) == cut;
@@ -284,65 +296,88 @@ __global__ void __launch_bounds__(THREADS) kv_evict_kernel(const __grid_constant
   }
 
   // ---- number the holes and the movers -------------------------------------
+  const bool near = cs == 1 && a.list_len <= kSmemList;
+  int4* const pages = near ? s.pages : a.pages + unit * a.list_len;   // (from page, row, to page, row); from page -1: not copied
+  int32_t* const to = near ? s.list : a.list + unit * 2 * a.list_len;
+  int32_t* const from = near ? s.list + kSmemList : to + a.list_len;
   auto stays = [&](int32_t j) {
     const uint32_t key = key_at(j);
     return key > cut || (key == cut && j <= cut_slot);
   };
-  int32_t holes = 0, moves = 0;
-  for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
-    const int32_t j = j0 + lane;
-    const bool in = j < w_end, st = in && stays(j);
-    holes += __popc(__ballot_sync(0xffffffffu, in && j < budget && !st));
-    moves += __popc(__ballot_sync(0xffffffffu, j >= budget && st));
-  }
-  __syncthreads();   // warp_a may still be read
-  if (lane == 0) {
-    s.warp_a[warp] = holes;
-    s.warp_b[warp] = moves;
-  }
-  __syncthreads();
-  int32_t hole_at = 0, move_at = 0, total = 0;
-  if (cs > 1) {
-    if (tid == 0) {
-      int32_t x = 0, y = 0;
-      for (int w = 0; w < WARPS; ++w) x += s.warp_a[w], y += s.warp_b[w];
-      s.cta_b = x;
-      s.count = (uint32_t)y;
-    }
-    cluster.sync();
+  int32_t total = 0;
+  if (one) {
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      const int32_t x = r < cs ? of(&s.cta_b, r) : 0, y = r < cs ? (int32_t)of(&s.count, r) : 0;
-      if (r < rank) {
-        hole_at += x;
-        move_at += y;
-      }
-      total += x;   // as many holes as movers: exactly `budget` slots stay
+    for (int o = 16; o >= 1; o >>= 1) {
+      const uint64_t x = __shfl_xor_sync(0xffffffffu, least, o);
+      least = x < least ? x : least;
     }
-  }
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) hole_at += s.warp_a[w], move_at += s.warp_b[w];
-    if (cs == 1) total += s.warp_a[w];
-  }
+    if (lane == 0) s.least[warp] = least;
+    sync();
+    for (int r = 0; r < cs; ++r)
+      for (int w = 0; w < WARPS; ++w) {
+        const uint64_t x = of(&s.least[w], r);
+        least = x < least ? x : least;
+      }
+    const int32_t out = (int32_t)~(uint32_t)least;
+    total = out < budget;   // the slot above the budget takes its place, or leaves itself
+    if (rank == 0 && tid == 0) {
+      if (total) {
+        to[0] = out;
+        from[0] = budget;
+      } else {
+        if (inplace) a.weights_out[base + budget] = 0.f;
+        if (pos_inplace) a.slot_pos_out[base + budget] = 0;
+      }
+    }
+  } else {
+    int32_t holes = 0, moves = 0;
+#pragma unroll 4
+    for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
+      const int32_t j = j0 + lane;
+      const bool in = j < w_end, st = in && stays(j);
+      holes += __popc(__ballot_sync(0xffffffffu, in && j < budget && !st));
+      moves += __popc(__ballot_sync(0xffffffffu, j >= budget && st));
+    }
+    __syncthreads();   // warp_a may still be read
+    if (lane == 0) {
+      s.warp_a[warp] = holes;
+      s.warp_b[warp] = moves;
+    }
+    __syncthreads();
+    const int32_t wa = lane < WARPS ? s.warp_a[lane] : 0, wb = lane < WARPS ? s.warp_b[lane] : 0;
+    int32_t hole_at = __reduce_add_sync(0xffffffffu, lane < warp ? wa : 0);
+    int32_t move_at = __reduce_add_sync(0xffffffffu, lane < warp ? wb : 0);
+    total = __reduce_add_sync(0xffffffffu, wa);   // as many holes as movers: exactly `budget` slots stay
+    if (cs > 1) {
+      const int32_t y = __reduce_add_sync(0xffffffffu, wb);
+      if (tid == 0) {
+        s.cta_a = total;
+        s.cta_b = y;
+      }
+      cluster.sync();
+      const int32_t ra = lane < cs ? *cluster.map_shared_rank(&s.cta_a, lane) : 0;
+      const int32_t rb = lane < rank ? *cluster.map_shared_rank(&s.cta_b, lane) : 0;
+      hole_at += __reduce_add_sync(0xffffffffu, lane < rank ? ra : 0);
+      move_at += __reduce_add_sync(0xffffffffu, rb);
+      total = __reduce_add_sync(0xffffffffu, ra);
+    }
 
-  // ---- list them ---------------------------------------------------------------
-  const bool near = cs == 1 && total <= kSmemList;
-  int4* const pages = near ? s.pages : a.pages + unit * a.list_len;   // (from page, row, to page, row); from page -1: not copied
-  int32_t* const to = near ? s.list : a.list + unit * 2 * a.list_len;
-  int32_t* const from = near ? s.list + kSmemList : to + a.list_len;
-  for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
-    const int32_t j = j0 + lane;
-    const uint32_t below = (1u << lane) - 1u;
-    const bool in = j < w_end, st = in && stays(j);
-    const bool hole = in && j < budget && !st, mover = st && j >= budget;
-    const uint32_t mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
-    if (hole) to[hole_at + __popc(mh & below)] = j;
-    if (mover) from[move_at + __popc(mm & below)] = j;
-    hole_at += __popc(mh);
-    move_at += __popc(mm);
-    if (in && j >= budget && !mover) {   // in place a mover's are cleared once they have been read
-      if (inplace) a.weights_out[base + j] = 0.f;
-      if (pos_inplace) a.slot_pos_out[base + j] = 0;
+    // ---- list them -------------------------------------------------------------
+#pragma unroll 4
+    for (int32_t j0 = (int32_t)w0; j0 < w_end; j0 += 32) {
+      const int32_t j = j0 + lane;
+      const uint32_t below = (1u << lane) - 1u;
+      const bool in = j < w_end, st = in && stays(j);
+      const bool hole = in && j < budget && !st, mover = st && j >= budget;
+      const uint32_t mh = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
+      if (hole) to[hole_at + __popc(mh & below)] = j;
+      if (mover) from[move_at + __popc(mm & below)] = j;
+      hole_at += __popc(mh);
+      move_at += __popc(mm);
+      if (in && j >= budget && !mover) {   // in place a mover's are cleared once they have been read
+        if (inplace) a.weights_out[base + j] = 0.f;
+        if (pos_inplace) a.slot_pos_out[base + j] = 0;
+      }
     }
   }
   sync();   // the lists are complete (and no CTA leaves while its counts are read)
@@ -426,16 +461,16 @@ static cudaError_t launch_threads(const Launch& L, KvEvictArgs& a, int cs) {
   return L.end(kKernelKvEvict);
 }
 
-// CTAs per (sequence, head) and their threads: enough for four CTAs of 256
-// threads on every SM, as long as a CTA keeps 512 slots; where even eight a head
-// leave SMs idle, CTAs of 1024 threads.
+// CTAs per (sequence, head) and their threads (64 registers each): all resident at
+// once.  Up to 296 units take 512 threads, and clusters of up to eight while a CTA
+// keeps 1024 slots and two CTAs an SM hold them all (clusters of 1024-thread CTAs
+// did not all find room in the GPU's processing clusters and ran in two waves).
 cudaError_t launch_kv_evict(const Launch& L, const KvEvictArgs& args) {
   KvEvictArgs a = args;
   const int64_t units = (int64_t)a.B * a.n_kv_heads;
   int cs = 1;
-  while (cs < kMaxCluster && a.max_len > 512 * cs && (units * cs * 2 <= 4 * 148 || a.max_len > (int64_t)kMaxCachedKeys * cs)) cs *= 2;
-  const bool wide = units * cs <= 148 && a.max_len > 1024 * cs;
-  cudaError_t e = wide ? launch_threads<1024>(L, a, cs) : launch_threads<256>(L, a, cs);
+  while (cs < kMaxCluster && a.max_len > 1024 * cs && (units * cs * 2 <= 296 || a.max_len > (int64_t)kMaxCachedKeys * cs)) cs *= 2;
+  cudaError_t e = units * cs <= 296 ? launch_threads<512>(L, a, cs) : launch_threads<256>(L, a, cs);
   if (e != cudaSuccess || a.lens_out != a.lens) return e;
   L.begin(kKernelKvEvict);
   kv_evict_lengths_kernel<<<(unsigned)((a.B + 255) / 256), 256, 0, L.stream>>>(a);
