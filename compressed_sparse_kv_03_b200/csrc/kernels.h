@@ -395,7 +395,7 @@ struct KvEvictArgs {
   int64_t max_len;
   int32_t* src_out;
   int32_t* list;                // [B * n_kv_heads][2][list_len]: holes, then the slots that fill them
-  int4* pages;                  // [B * n_kv_heads][list_len]: pages and rows of the listed slots
+  int32_t* moves;               // [B * n_kv_heads]: how many
   int64_t list_len;
   int32_t shared;               // 1: keys and values are the same memory
   int32_t key_cap;              // keys a CTA holds in shared memory (set by the launch)

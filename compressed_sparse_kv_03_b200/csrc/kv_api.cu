@@ -312,9 +312,9 @@ csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv
 
 size_t csa_kv_evict_workspace_size(int32_t B, int32_t n_kv_heads, int32_t budget, int64_t max_len) {
   if (B <= 0 || n_kv_heads < 1 || budget < 1 || max_len < 0) return kWsHeader;
-  // per move: the two slots, and their pages and rows
-  const size_t moves = (size_t)B * n_kv_heads * evict_list_len(budget, max_len);
-  return kWsHeader + align256(moves * 2 * sizeof(int32_t)) + align256(moves * sizeof(int4));
+  // the slots of every move, and the number of moves
+  const size_t units = (size_t)B * n_kv_heads;
+  return kWsHeader + align256(units * 2 * evict_list_len(budget, max_len) * sizeof(int32_t)) + align256(units * sizeof(int32_t));
 }
 
 csa_status_t csa_kv_evict(const csa_kv_cache_t* kv, const int32_t* lens, int32_t* lens_out,
@@ -372,8 +372,8 @@ csa_status_t csa_kv_evict(const csa_kv_cache_t* kv, const int32_t* lens, int32_t
   a.src_out = src_out;
   a.list = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kWsHeader);
   a.list_len = evict_list_len(budget, max_len);
-  a.pages = reinterpret_cast<int4*>(static_cast<char*>(ws) + kWsHeader +
-                                    align256((size_t)B * kv->n_kv_heads * 2 * a.list_len * sizeof(int32_t)));
+  a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kWsHeader +
+                                       align256((size_t)B * kv->n_kv_heads * 2 * a.list_len * sizeof(int32_t)));
   a.err = static_cast<WsHeader*>(ws);
   Launch L{(cudaStream_t)stream};
   return cuda_status(launch_kv_evict(L, a), "csa_kv_evict launch");

@@ -169,10 +169,10 @@ def test_evict_refuses_bad_arguments_without_launching(lib, mem):
     assert st(_13=9) == 1 and st(_13=-1) == 1
     assert st(_16=256) == 5
     assert st(_9=0) == 0
-    # per sequence and head min(max_len - budget, budget) moves: two slots, pages and rows
-    assert lib.csa_kv_evict_workspace_size(2, 8, 100, 90) == 256
-    assert lib.csa_kv_evict_workspace_size(2, 8, 100, 132) == 256 + 2 * 8 * 32 * 24
-    assert lib.csa_kv_evict_workspace_size(2, 8, 100, 10000) == 256 + 2 * 8 * 100 * 24
+    # per sequence and head min(max_len - budget, budget) moves, two slots each, and their number
+    assert lib.csa_kv_evict_workspace_size(2, 8, 100, 90) == 512
+    assert lib.csa_kv_evict_workspace_size(2, 8, 100, 132) == 512 + 2 * 8 * 2 * 32 * 4
+    assert lib.csa_kv_evict_workspace_size(2, 8, 100, 10000) == 512 + 12800
     assert lib.csa_launch_count() == before
 
 
