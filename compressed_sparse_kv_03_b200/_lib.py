@@ -14,6 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_csa_b200.so")
 
 CSA_OK = 0
+CSA_ERR_WORKSPACE = 5
 STATUS_NAMES = {0: "CSA_OK", 1: "CSA_ERR_INVALID_ARG", 2: "CSA_ERR_UNSUPPORTED", 3: "CSA_ERR_CUDA",
                 4: "CSA_ERR_DEVICE_CHECK", 5: "CSA_ERR_WORKSPACE"}
 

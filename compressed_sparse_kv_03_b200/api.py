@@ -23,7 +23,6 @@ or a shared-KV cache with k is v):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 from dataclasses import dataclass
 from typing import Optional
@@ -538,6 +537,7 @@ class KVCache:
                            None if page_table is None else page_table.data_ptr(), self.max_pages,
                            self.page_size, self.n_kv_heads, self.head_dim, _KV_DTYPES[k.dtype])
         self._ref = C.byref(self._c)
+        self._need = {}   # workspace sizes of the attention calls made so far
 
     @staticmethod
     def new(n_seq, max_len, n_kv_heads, head_dim, dtype=torch.bfloat16, device="cuda"):
@@ -565,7 +565,7 @@ def _kv_array(t, name, dtype, B, cache, slots=None):
     shape = (B,) if slots is None else (B, cache.n_kv_heads, slots)
     if t.dtype is not dtype or t.device != cache.device:
         raise TypeError(f"{name} must be {dtype} on {cache.device}, got {t.dtype} on {t.device}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -575,29 +575,28 @@ _kv_ws = {}
 
 def _kv_scratch(ws, dev, stream, nbytes):
     """Scratch of a call without a workspace of its own: one buffer per device
-    and stream, so that calls on two streams never share one; inside a stream
-    capture a buffer from the capture's own pool."""
+    and stream (a cudaStream_t as an int), so that calls on two streams never
+    share one; inside a stream capture a buffer from the capture's own pool."""
     if ws is None:
         if torch.cuda.is_current_stream_capturing():
             ws = Workspace(dev)
         else:
-            key = (dev.index, stream.cuda_stream)
-            ws = _kv_ws.get(key)
+            ws = _kv_ws.get((dev.index, stream))
             if ws is None:
-                ws = _kv_ws[key] = Workspace(dev)
+                ws = _kv_ws[(dev.index, stream)] = Workspace(dev)
     return ws.get(nbytes)
 
 
-@contextlib.contextmanager
-def _on(dev, stream):
-    """Run on `dev` and on `stream` (default: that device's current stream), so
-    that launches and allocations belong there."""
+def _kv_run(dev, stream, body):
+    """body(cudaStream_t) with `dev` current and on `stream` (default: that
+    device's current stream), so that launches and allocations belong there."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return body(torch._C._cuda_getCurrentRawStream(dev.index))
     with torch.cuda.device(dev):
         if stream is None:
-            yield torch.cuda.current_stream(dev)
-        else:
-            with torch.cuda.stream(stream):
-                yield stream
+            return body(torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.stream(stream):
+            return body(stream.cuda_stream)
 
 
 def kv_append(k_new, v_new, cache: KVCache, lens, *, token_start=None, pos=None, weights=None,
@@ -635,11 +634,13 @@ def kv_append(k_new, v_new, cache: KVCache, lens, *, token_start=None, pos=None,
             sp = _kv_array(slot_pos, "slot_pos", torch.int32, B, cache, slots)
     if pos is not None:
         pp = _kv_array(pos, "pos", torch.int32, B, cache)
-    with _on(cache.device, stream) as s:
+    tp = None if token_start is None else token_start.data_ptr()
+
+    def body(s):
         wsp, wsb = _kv_scratch(ws, cache.device, s, 256)
-        check(load().csa_kv_append(kr, vr, cache._ref, _ptr(token_start), T, B, lp, op, pp, wp, sp, slots,
-                                   wsp, wsb, s.cuda_stream))
-    return lens_out
+        check(load().csa_kv_append(kr, vr, cache._ref, tp, T, B, lp, op, pp, wp, sp, slots, wsp, wsb, s))
+        return lens_out
+    return _kv_run(cache.device, stream, body)
 
 
 def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0, sink=None,
@@ -671,18 +672,30 @@ def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0,
         _need(sink, "sink", torch.float32, 1, cache.device)
         if sink.shape[0] != H:
             raise ValueError("sink must be [H]")
-    lib = load()
-    with _on(cache.device, stream) as s:
-        if out is None:
-            out = torch.empty((B, H, cache.head_dim), dtype=cache.dtype, device=cache.device)
-        elif out.dtype is not cache.dtype or out.device != cache.device or out.shape != q.shape or not out.is_contiguous():
-            raise ValueError("out must be contiguous, with the shape and dtype of q")
-        lse = torch.empty((B, H), dtype=torch.float32, device=cache.device) if return_lse else None
-        need = lib.csa_kv_attn_decode_workspace_size(B, H, cache._ref, max_len, 0 if op is None else 1)
-        wsp, wsb = _kv_scratch(ws, cache.device, s, need)
-        check(lib.csa_kv_attn_decode(qr, cache._ref, lp, B, H, max_len, window, sm_scale, _ptr(sink),
-                                     out.data_ptr(), _ptr(lse), wp, op, slots, wsp, wsb, s.cuda_stream))
-    return (out, lse) if return_lse else out
+    zp = None if sink is None else sink.data_ptr()
+    if out is not None and (out.dtype is not cache.dtype or out.device != cache.device or out.shape != q.shape or
+                            not out.is_contiguous()):
+        raise ValueError("out must be contiguous, with the shape and dtype of q")
+
+    def body(s):
+        lib = load()
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device) if return_lse else None
+        key = (B, H, max_len, op is None)
+        need = cache._need.get(key)
+        for again in (True, False):
+            if need is None:
+                need = cache._need[key] = lib.csa_kv_attn_decode_workspace_size(B, H, cache._ref, max_len,
+                                                                               0 if op is None else 1)
+            wsp, wsb = _kv_scratch(ws, cache.device, s, need)
+            st = lib.csa_kv_attn_decode(qr, cache._ref, lp, B, H, max_len, window, sm_scale, zp, o.data_ptr(),
+                                        None if lse is None else lse.data_ptr(), wp, op, slots, wsp, wsb, s)
+            if st != _lib.CSA_ERR_WORKSPACE or not again:
+                break
+            need = None   # the size depends on csa_set_batch_invariant, which was called since
+        check(st)
+        return (o, lse) if return_lse else o
+    return _kv_run(cache.device, stream, body)
 
 
 def kv_evict(cache: KVCache, lens, weights, slot_pos, pos, budget, recent, *, keep_first=0,
@@ -710,14 +723,17 @@ def kv_evict(cache: KVCache, lens, weights, slot_pos, pos, budget, recent, *, ke
             _kv_array(slot_pos, "slot_pos", torch.int32, B, cache, slots),
             _kv_array(slot_pos_out, "slot_pos_out", torch.int32, B, cache, slots), slots,
             _kv_array(pos, "pos", torch.int32, B, cache))
-    lib = load()
-    with _on(cache.device, stream) as s:
-        src = torch.empty((B, cache.n_kv_heads, max(0, budget)), dtype=torch.int32, device=cache.device) if return_src else None
+
+    def body(s):
+        lib = load()
+        src = None
+        if return_src:
+            src = torch.empty((B, cache.n_kv_heads, max(0, budget)), dtype=torch.int32, device=cache.device)
         wsp, wsb = _kv_scratch(ws, cache.device, s,
                                lib.csa_kv_evict_workspace_size(B, cache.n_kv_heads, budget, max_len))
-        check(lib.csa_kv_evict(cache._ref, *args, B, budget, recent, keep_first, max_len, _ptr(src), wsp, wsb,
-                               s.cuda_stream))
-    return (lens_out, src) if return_src else lens_out
+        check(lib.csa_kv_evict(cache._ref, *args, B, budget, recent, keep_first, max_len, _ptr(src), wsp, wsb, s))
+        return (lens_out, src) if return_src else lens_out
+    return _kv_run(cache.device, stream, body)
 
 
 def launch_count():

@@ -812,7 +812,8 @@ bool tile_map(const char* data, int64_t page_st, int64_t slot_st, int64_t head_s
 template <class T, int DP, int NB, int WH>
 cudaError_t launch_typed(const Launch& L, const KvAttnArgs& args, const KvAttnPlan& p) {
   using Geo = Geometry<T, DP, NB, WH>;
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<T, DP, NB, WH>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::SMEM);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(kv_attn_kernel<T, DP, NB, WH>, Geo::SMEM, done);
   if (e != cudaSuccess) return e;
   KvAttnArgs a = args;
   CUtensorMap map_k = {}, map_v = {};

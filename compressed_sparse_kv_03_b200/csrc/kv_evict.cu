@@ -467,8 +467,8 @@ static cudaError_t launch_threads(const Launch& L, KvEvictArgs& a, int cs) {
   const int per = cs * THREADS;   // slots a run advances by
   const int64_t run = ((a.max_len + per / 32 - 1) / (per / 32) + 31) / 32 * 32 * (THREADS / 32);
   a.key_cap = (int32_t)(run <= kMaxCachedKeys ? run : kMaxCachedKeys);
-  cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMaxCachedKeys * (int)sizeof(uint32_t));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_shared(kv_evict_kernel<THREADS>, kMaxCachedKeys * (int)sizeof(uint32_t), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cs));
