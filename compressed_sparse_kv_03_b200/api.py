@@ -679,8 +679,9 @@ def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0,
 
     def body(s):
         lib = load()
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device) if return_lse else None
+        d = cache.head_dim
+        o = torch.empty_strided((B, H, d), (H * d, d, 1), dtype=cache.dtype, device=cache.device) if out is None else out
+        lse = torch.empty_strided((B, H), (H, 1), dtype=torch.float32, device=cache.device) if return_lse else None
         key = (B, H, max_len, op is None)
         need = cache._need.get(key)
         for again in (True, False):

@@ -38,6 +38,7 @@ constexpr int kThreads = 128;
 constexpr int kSms = 148;
 constexpr int kKeys = 16;            // keys of a step
 constexpr int kInvariantSlots = 512;
+constexpr int kMaxBlocks = 2;        // head blocks of a group: up to 128 heads, 64 at a time
 
 template <class T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -668,11 +669,82 @@ __device__ __forceinline__ float2 join_ml(float2 x, float2 y) {
   return make_float2(M, x.y * ex2(x.x - R) + y.y * ex2(y.x - R));
 }
 
-// Joins the pieces of the units that have several (or none: an empty
-// sequence; the attention kernel has written the others).  `split` of the
-// block's four warps share a head's pieces.
+// Slots of a weighing block: about 16 KB of scores.
+constexpr int weigh_slots(int G) { return G <= 16 ? 512 : 128; }
+
+// weights_out of one block of slots: the group's log-sum-exps from the pieces (or
+// from the attention kernel, for units of one piece), then the probabilities of
+// the scores, summed over the group in head order.  A lane takes four slots;
+// for up to 16 heads each warp has slots of its own, beyond that the four warps
+// take the heads of the same slots apart and their sums are added in warp order.
+template <int TILE, int ROWS>
+__device__ void weigh(const KvAttnArgs& a, int b, int kvh, int32_t n, int32_t s0, const Pieces* ps, int blocks) {
+  __shared__ float2 s_part[kThreads];
+  __shared__ float s_lse[128];
+  __shared__ float4 s_sum[4][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.H / a.n_kv_heads;
+  const int64_t bh = (int64_t)b * a.H + (int64_t)kvh * G;
+  const int row = tid % ROWS, part = tid / ROWS;
+  constexpr int PARTS = kThreads / ROWS;
+  for (int hb = 0; hb < blocks; ++hb) {
+    const int h = hb * ROWS + row;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (ps[hb].count > 1) {
+#pragma unroll 4
+      for (int64_t i = part; i < ps[hb].count; i += PARTS)
+        ml = join_ml(ml, *reinterpret_cast<const float2*>(a.part_ml + (ps[hb].at(i) * ROWS + row) * 2));
+      s_part[tid] = ml;
+      __syncthreads();
+      if (part == 0)
+        for (int w = 1; w < PARTS; ++w) ml = join_ml(ml, s_part[w * ROWS + row]);
+      __syncthreads();
+    }
+    if (part == 0 && h < G) {
+      const float e = ps[hb].count > 1 ? normalise(ml.x, ml.y, a.sink ? a.sink[kvh * G + h] * kLog2e : -INFINITY).lse2
+                                       : a.lse2[bh + h];
+      s_lse[h] = e == -INFINITY ? INFINITY : e;   // a head without any weight (every slot on a bad page) adds nothing
+    }
+  }
+  __syncthreads();
+  const int64_t at = ((int64_t)b * a.n_kv_heads + kvh) * a.slots;
+  const bool split = G > 16;
+  const int32_t s = s0 + (split ? 0 : warp * 128) + 4 * lane;
+  const float* const sc = a.scores + bh * a.score_stride + s;
+  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (s < n) {   // a row of scores ends on a multiple of 32
+#pragma unroll 8
+    for (int h = split ? warp : 0; h < G; h += split ? 4 : 1) {
+      const float4 z = *reinterpret_cast<const float4*>(sc + h * a.score_stride);
+      const float e = s_lse[h];
+      w.x += ex2(z.x - e);
+      w.y += ex2(z.y - e);
+      w.z += ex2(z.z - e);
+      w.w += ex2(z.w - e);
+    }
+  }
+  s_sum[warp][lane] = w;
+  const float* const sum = reinterpret_cast<const float*>(s_sum);
+  if (split) __syncthreads();
+  else __syncwarp();
+  // slots in lane order again: rows of weights need not be aligned
+  const int32_t first = split ? s0 + tid : s0 + warp * 128 + lane;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (split && i > 0) break;
+    const int32_t j = first + i * 32;
+    if (j >= n) break;
+    const float v = split ? (sum[tid] + sum[128 + tid]) + (sum[256 + tid] + sum[384 + tid]) : sum[warp * 128 + i * 32 + lane];
+    a.weights_out[at + j] = a.weights ? a.weights[at + j] + v : v;
+  }
+}
+
+// Blocks x < join_blocks join the pieces of the units that have several (or
+// none: an empty sequence; the attention kernel has written the others);
+// `split` of the block's four warps share a head's pieces.  The other blocks, with
+// weights_out, weigh.
 template <class T, int DP, int NB, int WH>
-__global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant__ KvAttnArgs a, int split) {
+__global__ void __launch_bounds__(kThreads) kv_finish_kernel(const __grid_constant__ KvAttnArgs a, int join_blocks, int split) {
   using Geo = Geometry<T, DP, NB, WH>;
   constexpr int ROWS = Geo::HEADS, V = DP / 64;   // float2 per lane
   __shared__ int64_t s_scan[4];
@@ -681,9 +753,22 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
   const int b = blockIdx.z, kvh = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.H / a.n_kv_heads, blocks = (G + ROWS - 1) / ROWS, HZ = a.n_kv_heads * blocks;
+  // the lengths do not come from the attention kernel: read them while it runs
+  if ((int)blockIdx.x >= join_blocks) {
+    const int32_t n = kv_clamp_len(__ldg(a.lens + b), a.max_len, b, nullptr);
+    const int32_t s0 = (blockIdx.x - join_blocks) * weigh_slots(G);
+    Pieces ps[kMaxBlocks];
+    if (s0 < n)
+#pragma unroll
+      for (int hb = 0; hb < kMaxBlocks; ++hb)
+        ps[hb] = a.whole || hb >= blocks ? Pieces{0, 0, 1, 0} : pieces_of<Geo::TILE>(a, b, HZ, kvh * blocks + hb, s_scan);
+    pdl_wait();
+    pdl_trigger();
+    if (s0 < n) weigh<Geo::TILE, ROWS>(a, b, kvh, n, s0, ps, blocks);
+    return;
+  }
   const int first = blockIdx.x * (4 / split);   // 4 / split heads, in one head block
   const int hb = first / ROWS;
-  // the lengths do not come from the attention kernel: read them while it runs
   const Pieces ps = pieces_of<Geo::TILE>(a, b, HZ, kvh * blocks + hb, s_scan);
   pdl_wait();
   pdl_trigger();
@@ -740,57 +825,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const __grid_constant
   for (int j = 0; j < V; ++j)
     if (j * 64 + 2 * lane < a.d)
       *reinterpret_cast<uint32_t*>(a.out + (bh * a.d + j * 64 + 2 * lane) * 2) = pack2<T>(acc[j].x * nm.scale, acc[j].y * nm.scale);
-  if (lane == 0) {
-    if (a.lse) a.lse[bh] = nm.lse2 * (1.f / kLog2e);
-    if (a.lse2) a.lse2[bh] = nm.lse2;
-  }
-}
-
-// weights_out: the probabilities of the scores, summed over the group.  128
-// slots at a time, four to a lane; the four warps take the group's heads apart
-// and their sums are added in warp order.
-__global__ void __launch_bounds__(kThreads) kv_weigh_kernel(const __grid_constant__ KvAttnArgs a, int slots_per_block) {
-  __shared__ float s_lse[128];
-  __shared__ float4 s_sum[4][32];
-  const int b = blockIdx.z, kvh = blockIdx.y;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.H / a.n_kv_heads;
-  const int64_t bh = (int64_t)b * a.H + (int64_t)kvh * G;
-  const int32_t n = kv_clamp_len(__ldg(a.lens + b), a.max_len, b, nullptr);
-  const int32_t s0 = blockIdx.x * slots_per_block;
-  pdl_wait();
-  pdl_trigger();
-  if (s0 >= n) return;
-  if (tid < G) {   // a head without any weight (every slot on a bad page) adds nothing
-    const float e = a.lse2[bh + tid];
-    s_lse[tid] = e == -INFINITY ? INFINITY : e;
-  }
-  __syncthreads();
-  const int64_t at = ((int64_t)b * a.n_kv_heads + kvh) * a.slots;
-  const int32_t end = s0 + slots_per_block < n ? s0 + slots_per_block : n;
-  for (int32_t s = s0; s < end; s += 128) {
-    const float* const sc = a.scores + bh * a.score_stride + s + 4 * lane;
-    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (s + 4 * lane < end) {   // a row of scores ends on a multiple of 4
-#pragma unroll 8
-      for (int h = warp; h < G; h += 4) {
-        const float4 z = *reinterpret_cast<const float4*>(sc + h * a.score_stride);
-        const float e = s_lse[h];
-        w.x += ex2(z.x - e);
-        w.y += ex2(z.y - e);
-        w.z += ex2(z.z - e);
-        w.w += ex2(z.w - e);
-      }
-    }
-    s_sum[warp][lane] = w;
-    __syncthreads();
-    if (s + tid < end) {
-      const float* const sum = reinterpret_cast<const float*>(s_sum);
-      const float v = (sum[tid] + sum[128 + tid]) + (sum[256 + tid] + sum[384 + tid]);
-      a.weights_out[at + s + tid] = a.weights ? a.weights[at + s + tid] + v : v;
-    }
-    __syncthreads();
-  }
+  if (lane == 0 && a.lse) a.lse[bh] = nm.lse2 * (1.f / kLog2e);
 }
 
 // Tensor map of a cache's keys or values, [page][slot][head][coordinate], if 16
@@ -824,22 +859,15 @@ cudaError_t launch_typed(const Launch& L, const KvAttnArgs& args, const KvAttnPl
                     map_v, a);
   if (e != cudaSuccess) return e;
   e = L.end(kKernelAttention);
-  if (e != cudaSuccess || p.whole) return e;
+  if (e != cudaSuccess || (p.whole && a.weights_out == nullptr)) return e;
   const int G = a.H / a.n_kv_heads;
   const int split = (int64_t)a.B * a.n_kv_heads * p.blocks * 4 > p.n_ctas ? 1 : 4;   // 4 where a unit has many pieces
+  const int join = p.whole ? 0 : (G * split + 3) / 4;
+  const int weigh = a.weights_out ? (int)((a.max_len + weigh_slots(G) - 1) / weigh_slots(G)) : 0;
+  if (join + weigh == 0) return cudaSuccess;
   L.begin(kKernelMerge);
-  e = launch_kernel(kv_join_kernel<T, DP, NB, WH>, dim3((unsigned)((G * split + 3) / 4), (unsigned)a.n_kv_heads, (unsigned)a.B),
-                    dim3(kThreads), 0, L.stream, true, a, split);
-  if (e != cudaSuccess) return e;
-  return L.end(kKernelMerge);
-}
-
-cudaError_t launch_weigh(const Launch& L, const KvAttnArgs& a) {
-  const int G = a.H / a.n_kv_heads;
-  const int per = G <= 8 ? 512 : G <= 16 ? 256 : 128;   // about 16 KB of scores a block
-  L.begin(kKernelMerge);
-  const cudaError_t e = launch_kernel(kv_weigh_kernel, dim3((unsigned)((a.max_len + per - 1) / per), (unsigned)a.n_kv_heads, (unsigned)a.B),
-                                      dim3(kThreads), 0, L.stream, true, a, per);
+  e = launch_kernel(kv_finish_kernel<T, DP, NB, WH>, dim3((unsigned)(join + weigh), (unsigned)a.n_kv_heads, (unsigned)a.B),
+                    dim3(kThreads), 0, L.stream, true, a, join, split);
   if (e != cudaSuccess) return e;
   return L.end(kKernelMerge);
 }
@@ -892,9 +920,7 @@ KvAttnPlan kv_attn_plan(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int
 }
 
 cudaError_t launch_kv_attn(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p) {
-  const cudaError_t e = a.dtype == CSA_KV_FP16 ? launch_dp<__half>(L, a, p) : launch_dp<__nv_bfloat16>(L, a, p);
-  if (e != cudaSuccess || a.weights_out == nullptr || a.max_len == 0) return e;
-  return launch_weigh(L, a);
+  return a.dtype == CSA_KV_FP16 ? launch_dp<__half>(L, a, p) : launch_dp<__nv_bfloat16>(L, a, p);
 }
 
 }  // namespace csa
