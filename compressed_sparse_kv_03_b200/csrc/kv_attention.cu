@@ -669,7 +669,7 @@ __device__ __forceinline__ float2 join_ml(float2 x, float2 y) {
   return make_float2(M, x.y * ex2(x.x - R) + y.y * ex2(y.x - R));
 }
 
-// Slots of a weighing block: about 16 KB of scores.
+// Slots that a weighing block takes at a time: about 16 KB of scores.
 constexpr int weigh_slots(int G) { return G <= 16 ? 512 : 128; }
 
 // weights_out of one block of slots: the group's log-sum-exps from the pieces (or
@@ -678,7 +678,7 @@ constexpr int weigh_slots(int G) { return G <= 16 ? 512 : 128; }
 // for up to 16 heads each warp has slots of its own, beyond that the four warps
 // take the heads of the same slots apart and their sums are added in warp order.
 template <int TILE, int ROWS>
-__device__ void weigh(const KvAttnArgs& a, int b, int kvh, int32_t n, int32_t s0, const Pieces* ps, int blocks) {
+__device__ void weigh(const KvAttnArgs& a, int b, int kvh, int32_t n, int32_t s0, int32_t end, const Pieces* ps, int blocks) {
   __shared__ float2 s_part[kThreads];
   __shared__ float s_lse[128];
   __shared__ float4 s_sum[4][32];
@@ -709,33 +709,39 @@ __device__ void weigh(const KvAttnArgs& a, int b, int kvh, int32_t n, int32_t s0
   __syncthreads();
   const int64_t at = ((int64_t)b * a.n_kv_heads + kvh) * a.slots;
   const bool split = G > 16;
-  const int32_t s = s0 + (split ? 0 : warp * 128) + 4 * lane;
-  const float* const sc = a.scores + bh * a.score_stride + s;
-  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (s < n) {   // a row of scores ends on a multiple of 32
-#pragma unroll 8
-    for (int h = split ? warp : 0; h < G; h += split ? 4 : 1) {
-      const float4 z = *reinterpret_cast<const float4*>(sc + h * a.score_stride);
-      const float e = s_lse[h];
-      w.x += ex2(z.x - e);
-      w.y += ex2(z.y - e);
-      w.z += ex2(z.z - e);
-      w.w += ex2(z.w - e);
-    }
-  }
-  s_sum[warp][lane] = w;
-  const float* const sum = reinterpret_cast<const float*>(s_sum);
-  if (split) __syncthreads();
-  else __syncwarp();
-  // slots in lane order again: rows of weights need not be aligned
-  const int32_t first = split ? s0 + tid : s0 + warp * 128 + lane;
+  if (end > n) end = n;
+  for (; s0 < end; s0 += weigh_slots(G)) {
+    const int32_t s = s0 + (split ? 0 : warp * 128) + 4 * lane;
+    const float* const sc = a.scores + bh * a.score_stride + s;
+    // slots in lane order: rows of weights need not be aligned
+    const int32_t first = split ? s0 + tid : s0 + warp * 128 + lane;
+    const int mine = split ? 1 : 4;
+    float old[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (split && i > 0) break;
-    const int32_t j = first + i * 32;
-    if (j >= n) break;
-    const float v = split ? (sum[tid] + sum[128 + tid]) + (sum[256 + tid] + sum[384 + tid]) : sum[warp * 128 + i * 32 + lane];
-    a.weights_out[at + j] = a.weights ? a.weights[at + j] + v : v;
+    for (int i = 0; i < 4; ++i) old[i] = a.weights && i < mine && first + i * 32 < end ? a.weights[at + first + i * 32] : 0.f;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s < end) {   // a row of scores ends on a multiple of 32
+#pragma unroll 8
+      for (int h = split ? warp : 0; h < G; h += split ? 4 : 1) {
+        const float4 z = *reinterpret_cast<const float4*>(sc + h * a.score_stride);
+        const float e = s_lse[h];
+        w.x += ex2(z.x - e);
+        w.y += ex2(z.y - e);
+        w.z += ex2(z.z - e);
+        w.w += ex2(z.w - e);
+      }
+    }
+    s_sum[warp][lane] = w;
+    const float* const sum = reinterpret_cast<const float*>(s_sum);
+    if (split) __syncthreads();
+    else __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = split ? (sum[tid] + sum[128 + tid]) + (sum[256 + tid] + sum[384 + tid]) : sum[warp * 128 + i * 32 + lane];
+      if (i < mine && first + i * 32 < end) a.weights_out[at + first + i * 32] = old[i] + v;
+    }
+    if (split) __syncthreads();
+    else __syncwarp();
   }
 }
 
@@ -744,7 +750,7 @@ __device__ void weigh(const KvAttnArgs& a, int b, int kvh, int32_t n, int32_t s0
 // `split` of the block's four warps share a head's pieces.  The other blocks, with
 // weights_out, weigh.
 template <class T, int DP, int NB, int WH>
-__global__ void __launch_bounds__(kThreads) kv_finish_kernel(const __grid_constant__ KvAttnArgs a, int join_blocks, int split) {
+__global__ void __launch_bounds__(kThreads) kv_finish_kernel(const __grid_constant__ KvAttnArgs a, int join_blocks, int split, int weigh_per) {
   using Geo = Geometry<T, DP, NB, WH>;
   constexpr int ROWS = Geo::HEADS, V = DP / 64;   // float2 per lane
   __shared__ int64_t s_scan[4];
@@ -756,7 +762,7 @@ __global__ void __launch_bounds__(kThreads) kv_finish_kernel(const __grid_consta
   // the lengths do not come from the attention kernel: read them while it runs
   if ((int)blockIdx.x >= join_blocks) {
     const int32_t n = kv_clamp_len(__ldg(a.lens + b), a.max_len, b, nullptr);
-    const int32_t s0 = (blockIdx.x - join_blocks) * weigh_slots(G);
+    const int32_t s0 = (blockIdx.x - join_blocks) * weigh_per;
     Pieces ps[kMaxBlocks];
     if (s0 < n)
 #pragma unroll
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(kThreads) kv_finish_kernel(const __grid_consta
         ps[hb] = a.whole || hb >= blocks ? Pieces{0, 0, 1, 0} : pieces_of<Geo::TILE>(a, b, HZ, kvh * blocks + hb, s_scan);
     pdl_wait();
     pdl_trigger();
-    if (s0 < n) weigh<Geo::TILE, ROWS>(a, b, kvh, n, s0, ps, blocks);
+    if (s0 < n) weigh<Geo::TILE, ROWS>(a, b, kvh, n, s0, s0 + weigh_per, ps, blocks);
     return;
   }
   const int first = blockIdx.x * (4 / split);   // 4 / split heads, in one head block
@@ -863,11 +869,15 @@ cudaError_t launch_typed(const Launch& L, const KvAttnArgs& args, const KvAttnPl
   const int G = a.H / a.n_kv_heads;
   const int split = (int64_t)a.B * a.n_kv_heads * p.blocks * 4 > p.n_ctas ? 1 : 4;   // 4 where a unit has many pieces
   const int join = p.whole ? 0 : (G * split + 3) / 4;
-  const int weigh = a.weights_out ? (int)((a.max_len + weigh_slots(G) - 1) / weigh_slots(G)) : 0;
+  // weighing blocks long enough that about eight an SM do it all: each first
+  // finds its unit's pieces and sums (32 sequences of up to 8192 slots, 8 heads a group: 26 -> 19 us)
+  const int64_t total = (int64_t)a.B * a.n_kv_heads * a.max_len / (8 * kSms) + 1;
+  const int weigh_per = (int)((total + weigh_slots(G) - 1) / weigh_slots(G)) * weigh_slots(G);
+  const int weigh = a.weights_out ? (int)((a.max_len + weigh_per - 1) / weigh_per) : 0;
   if (join + weigh == 0) return cudaSuccess;
   L.begin(kKernelMerge);
   e = launch_kernel(kv_finish_kernel<T, DP, NB, WH>, dim3((unsigned)(join + weigh), (unsigned)a.n_kv_heads, (unsigned)a.B),
-                    dim3(kThreads), 0, L.stream, true, a, join, split);
+                    dim3(kThreads), 0, L.stream, true, a, join, split, weigh_per);
   if (e != cudaSuccess) return e;
   return L.end(kKernelMerge);
 }
