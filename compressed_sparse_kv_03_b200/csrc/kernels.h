@@ -450,6 +450,7 @@ struct KvAttnArgs {
 };
 // Geometry of a call, shared by the workspace size and the launch.
 struct KvAttnPlan {
+  int box_rows;                 // > 0: the tcgen05 kernel, with TMA boxes of so many rows
   int nb, wh;                   // blocks of 8 heads per warp, warps side by side in a CTA
   int heads;                    // of a unit: 8 nb wh
   int blocks;                   // head blocks of a group
@@ -458,8 +459,10 @@ struct KvAttnPlan {
   int runs, n_ctas, whole, atom;
   int64_t max_atoms, pieces;    // pieces: partial results that may exist
 };
-KvAttnPlan kv_attn_plan(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int64_t max_len, int32_t window,
-                        bool invariant);
+KvAttnPlan kv_attn_plan(const KvRef& kv, int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int64_t max_len,
+                        int32_t window, bool invariant);
+int kv_attn_tc_box_rows(const KvRef& kv, int32_t n_kv_heads);
+cudaError_t launch_kv_attn_tc(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p);
 cudaError_t launch_kv_attn(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p);
 
 // Whether csa_set_batch_invariant(1) is in force.

@@ -146,10 +146,9 @@ struct AttnLayout {
   int64_t score_stride;
   size_t ml_off, acc_off, lse_off, score_off, total;
 };
-AttnLayout attn_layout(int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int64_t max_len, int32_t window,
-                       bool weights) {
+AttnLayout attn_layout(const csa_kv_cache_t* kv, int32_t B, int32_t H, int64_t max_len, int32_t window, bool weights) {
   AttnLayout l;
-  l.plan = kv_attn_plan(B, H, n_kv_heads, d, max_len, window, batch_invariant());
+  l.plan = kv_attn_plan(to_ref(kv), B, H, kv->n_kv_heads, kv->head_dim, max_len, window, batch_invariant());
   const size_t rows = (size_t)l.plan.pieces * l.plan.heads;
   l.ml_off = kWsHeader;
   l.acc_off = l.ml_off + align256(rows * 2 * sizeof(float));
@@ -236,7 +235,7 @@ size_t csa_kv_attn_decode_workspace_size(int32_t B, int32_t H, const csa_kv_cach
       max_len < 0 || max_len > kMaxSlots)
     return kWsHeader;
   // a window only ever needs less
-  return attn_layout(B, H, kv->n_kv_heads, kv->head_dim, max_len, 0, with_weights != 0).total;
+  return attn_layout(kv, B, H, max_len, 0, with_weights != 0).total;
 }
 
 csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv,
@@ -272,7 +271,7 @@ csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv
       return fail(CSA_ERR_INVALID_ARG, "%s: weights_out must be weights or apart from it", name);
   }
   const bool weigh = weights_out != nullptr;
-  const AttnLayout l = attn_layout(B, H, kv->n_kv_heads, kv->head_dim, max_len, window, weigh);
+  const AttnLayout l = attn_layout(kv, B, H, max_len, window, weigh);
   if ((st = check_ws(ws, ws_bytes, l.total, name)) != CSA_OK) return st;
   KvAttnArgs a{};
   a.kv = to_ref(kv);

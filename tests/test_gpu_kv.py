@@ -107,7 +107,7 @@ def check_attend(cache, table, q, lens, scale, window=0, sink=None, weigh=False,
     assert not bad.any(), f"output: {bad.sum()} of {bad.size}, worst {np.max(np.abs(go - ro) - to):.3g}"
     empty = np.isinf(rl)
     assert np.array_equal(np.isneginf(gl), empty)
-    assert np.all(np.abs(gl - rl)[~empty] <= tl[~empty] + 4 * E * np.abs(rl[~empty]))
+    assert np.all(np.abs(gl[~empty] - rl[~empty]) <= tl[~empty] + 4 * E * np.abs(rl[~empty]))
     if weigh:
         gw = f64(wo)
         for b in range(B):
@@ -133,6 +133,13 @@ ATTEND = [
     (2, 64, 2, 64, [100, 1100], 32, "head"),
     (2, 64, 1, 128, [1000, 777], 64, "token"),           # 64 heads: four
     (1, 128, 1, 128, [900], 16, "token"),                # 128: two head blocks
+    (3, 51, 3, 96, [1, 300, 511], 48, "interleaved"),    # 17 heads on the tensor cores, boxes of 16 rows
+    (3, 66, 2, 64, [257, 640, 0], 128, "token"),         # 33 heads, boxes of 128
+    (2, 64, 1, 8, [700, 129], 0, "token"),
+    (2, 40, 1, 72, [100, 255], 0, "head"),               # a CTA per sequence
+    (2, 200, 2, 128, [1500, 130], 32, "head"),           # 100 heads: two blocks
+    (5, 64, 1, 128, [9000, 1, 128, 127, 129], 256, "token"),
+    (2, 64, 1, 128, [600, 200], 9, "token"),             # pages without a 16-row box
     (2, 100, 1, 192, [400, 33], 7, "token"),
     (2, 12, 3, 192, [333, 2], 64, "token"),
     (2, 16, 4, 256, [450, 31], 100, "token"),
@@ -157,20 +164,22 @@ def test_attention_matches_oracle(case, dtype):
 
 
 @pytest.mark.parametrize("sink", [False, True])
-@pytest.mark.parametrize("window", [1, 15, 16, 100, 5000])
-def test_attention_window_and_sink(window, sink):
+@pytest.mark.parametrize("G", [8, 20, 40])
+@pytest.mark.parametrize("window", [1, 15, 16, 100, 128, 500, 5000])
+def test_attention_window_and_sink(window, G, sink):
     g = torch.Generator().manual_seed(12)
     lens = [0, 1, 16, 99, 250, 1001]
     for page in (16, 7):
         cache, table = make_cache(g, 6, 1001, page, 2, 128)
-        q = (2 * torch.randn(6, 16, 128, generator=g)).bfloat16().cuda()
-        check_attend(cache, table, q, lens, 0.09, window=window, sink=torch.randn(16, generator=g) * 3 if sink else None)
+        q = (2 * torch.randn(6, 2 * G, 128, generator=g)).bfloat16().cuda()
+        check_attend(cache, table, q, lens, 0.09, window=window, sink=torch.randn(2 * G, generator=g) * 3 if sink else None)
 
 
 @pytest.mark.parametrize("inplace", [False, True])
 @pytest.mark.parametrize("case", [(3, 8, 2, 128, [40, 0, 64], 16), (3, 16, 2, 64, [900, 1, 333], 16),
                                   (2, 34, 2, 128, [1500, 20], 64), (2, 64, 1, 128, [1030, 600], 64),
-                                  (2, 128, 1, 64, [300, 1200], 5), (40, 4, 4, 96, None, 0)],
+                                  (2, 128, 1, 64, [300, 1200], 5), (40, 4, 4, 96, None, 0), (3, 96, 1, 128, [200, 1, 3000], 32),
+                                  (2, 40, 2, 64, [129, 900], 16), (2, 32, 1, 128, [100, 255], 0)],
                          ids=lambda c: "-".join(str(x) for x in c[:4]))
 def test_accumulated_weights(case, inplace):
     B, H, Hkv, d, lens, page = case
@@ -198,7 +207,7 @@ def test_weights_without_an_input_start_at_zero():
     assert torch.allclose(wo[0, :, :500].sum(-1), torch.full((2,), 4.0, device="cuda"), atol=1e-4)
 
 
-@pytest.mark.parametrize("G", [1, 16, 40])
+@pytest.mark.parametrize("G", [1, 16, 32, 40])
 def test_masked_slots_are_never_read(G):
     """Infinities and NaN in free slots, in other pages and before the window."""
     g = torch.Generator().manual_seed(15)
@@ -225,14 +234,31 @@ def test_masked_slots_are_never_read(G):
     assert torch.isfinite(out[1]).all()
 
 
-def test_nan_of_a_seen_slot_reaches_the_output():
+@pytest.mark.parametrize("G", [2, 24, 64])
+def test_nan_of_a_seen_slot_reaches_the_output(G):
     import compressed_sparse_kv_03_b200 as csa
     g = torch.Generator().manual_seed(16)
-    cache, table = make_cache(g, 2, 100, 16, 2, 64)
+    cache, table = make_cache(g, 2, 300, 16, 2, 64)
     cache.k[table[0, 3], 1, 0, 5] = float("nan")
-    q = torch.randn(2, 4, 64, generator=g).bfloat16().cuda()
-    out = csa.kv_attn_decode(q, cache, torch.tensor([100, 100], dtype=torch.int32, device="cuda"), 0.1)
-    assert torch.isnan(out[0, :2]).all() and torch.isfinite(out[0, 2:]).all() and torch.isfinite(out[1]).all()
+    q = torch.randn(2, 2 * G, 64, generator=g).bfloat16().cuda()
+    out = csa.kv_attn_decode(q, cache, torch.tensor([300, 300], dtype=torch.int32, device="cuda"), 0.1)
+    assert torch.isnan(out[0, :G]).all() and torch.isfinite(out[0, G:]).all() and torch.isfinite(out[1]).all()
+
+
+@pytest.mark.parametrize("G", [4, 24, 64])
+def test_scores_that_grow_along_the_cache(G):
+    """Every block of slots scores far above the ones before it, so the running
+    maximum moves again and again (and once, in the last block, downwards)."""
+    g = torch.Generator().manual_seed(31)
+    n, d = 1500, 128
+    cache, table = make_cache(g, 2, n, 64, 1, d)
+    q = torch.randn(2, G, d, generator=g).abs().bfloat16().cuda()
+    level = (torch.arange(n) // 100).float() * 0.05
+    level[-100:] = -0.3
+    for b in range(2):
+        for s in range(n):
+            cache.k[table[b, s // 64], s % 64] += level[s]
+    check_attend(cache, table, q, [n, 1023], 1.0, weigh=True)
 
 
 def test_shared_key_value_memory_and_strided_queries():
@@ -257,11 +283,12 @@ def test_equal_scores_and_a_dominant_slot():
     assert abs(float(lse[0, 0]) - 256) < 1e-3
 
 
-def test_bad_lengths_and_pages_are_recorded():
+@pytest.mark.parametrize("H", [4, 48, 80])
+def test_bad_lengths_and_pages_are_recorded(H):
     import compressed_sparse_kv_03_b200 as csa
     g = torch.Generator().manual_seed(19)
     cache, table = make_cache(g, 3, 160, 16, 2, 64)
-    q = torch.randn(3, 4, 64, generator=g).bfloat16().cuda()
+    q = torch.randn(3, H, 64, generator=g).bfloat16().cuda()
     ws = csa.Workspace("cuda")
     lens = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
     good = csa.kv_attn_decode(q, cache, lens(160, 100, 7), 0.1, ws=ws)
@@ -285,12 +312,13 @@ def test_bad_lengths_and_pages_are_recorded():
         assert torch.equal(out[0], good[0]) and torch.equal(out[2], good[2])
 
 
-def test_runs_are_bit_identical_and_batch_invariant_mode():
+@pytest.mark.parametrize("G", [8, 40])
+def test_runs_are_bit_identical_and_batch_invariant_mode(G):
     import compressed_sparse_kv_03_b200 as csa
     g = torch.Generator().manual_seed(20)
     lens = [3000, 1, 0, 511, 512, 513, 1400]
     cache, table = make_cache(g, 7, 3000, 64, 2, 128)
-    q = torch.randn(7, 16, 128, generator=g).bfloat16().cuda()
+    q = torch.randn(7, 2 * G, 128, generator=g).bfloat16().cuda()
     dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
     a = csa.kv_attn_decode(q, cache, dl, 0.09, return_lse=True)
     b = csa.kv_attn_decode(q, cache, dl, 0.09, return_lse=True)
