@@ -303,9 +303,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       bool alive = true;
       for (; c.tile < c.end; ++c.tile, ++tile) {
         const uint32_t sb = (uint32_t)(tile & 1);
-        const int64_t nk = tile * uses, nv = nk + uses - 1;
+        const int64_t nv = tile * uses + uses - 1;
+        // The values' slot stays filled until this tile's product, so its phase can
+        // still be asked for here (the keys' may have been filled again by now).
         bool ok = mbar_wait(smem_u32(&s_full[sb]), (uint32_t)((tile >> 1) & 1)) &&
-                  mbar_wait(smem_u32(&kv_full[ring_slot(nk, SLOTS)]), ring_phase(nk, SLOTS));
+                  mbar_wait(smem_u32(&kv_full[ring_slot(nv, SLOTS)]), ring_phase(nv, SLOTS));
         float y[HW];
         __syncwarp();
         tc::fence_after_sync();
@@ -411,7 +413,6 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                        : "memory");
         }
         if (grp == 0 && !seen) {   // 0 times what lies in an unseen value row may be NaN
-          if (!mbar_wait(smem_u32(&kv_full[ring_slot(nv, SLOTS)]), ring_phase(nv, SLOTS))) fail(7);
           const uint32_t v = kv_sm + ring_slot(nv, SLOTS) * Geo::SLOT + row * 128;
           for (int i = 0; i < BOXES * 8; ++i)
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(v + (i >> 3) * kBlock + (i & 7) * 16), "r"(0u) : "memory");

@@ -140,6 +140,9 @@ ATTEND = [
     (2, 200, 2, 128, [1500, 130], 32, "head"),           # 100 heads: two blocks
     (5, 64, 1, 128, [9000, 1, 128, 127, 129], 256, "token"),
     (2, 64, 1, 128, [600, 200], 9, "token"),             # pages without a 16-row box
+    (2, 280, 8, 128, [30000, 5000], 16, "token"),        # 16 tiles of 128 slots a CTA, and 17
+    (1, 272, 16, 64, [20000], 64, "head"),
+    (2, 64, 32, 128, [5000, 4000], 64, "token"),         # many tiles a CTA on mma.sync as well
     (2, 100, 1, 192, [400, 33], 7, "token"),
     (2, 12, 3, 192, [333, 2], 64, "token"),
     (2, 16, 4, 256, [450, 31], 100, "token"),
@@ -267,6 +270,9 @@ def test_shared_key_value_memory_and_strided_queries():
     qkv = torch.randn(3, 70, 128, generator=g).bfloat16().cuda()
     check_attend(cache, table, qkv[:, 2:66], [700, 64, 5], 0.088)
     check_attend(cache, table, qkv[:, 1:65:4], [700, 64, 5], 0.088, weigh=True)
+    cache, table = make_cache(g, 1, 12000, 64, 8, 64, shared=True)      # several tiles a CTA on one copy
+    q = torch.randn(1, 8 * 40, 64, generator=g).bfloat16().cuda()
+    check_attend(cache, table, q, [12000], 0.125)
 
 
 def test_equal_scores_and_a_dominant_slot():
