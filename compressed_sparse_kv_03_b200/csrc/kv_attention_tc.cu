@@ -105,6 +105,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   const int64_t hq = (int64_t)kvh * G;
   const int uses = shared_kv ? 1 : 2;   // ring slots of a tile
 
+  if (warp == kLoadWarp && lane < 2) tc::prefetch_tmap(lane == 0 ? &map_k : &map_v);
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(smem_u32(&kv_full[i]), 1);
@@ -138,6 +139,33 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   Cursor c;
   bool more = begin_run<kKeys, kKeys, kThreads>(a, run, c, s_scan, s_first);
   bool continued = more && c.tile > 0;   // the unit began before this run
+
+  // Query heads of a segment into the swizzled tile, by `n` threads.  Row r of the
+  // tile: head r of group 0, r - 32 of group 1, HW of each.  Rolled, as all that
+  // runs once: its instructions come from a cold cache.
+  constexpr int kPieces = HEADS * BOXES * 8;   // of 16 bytes
+  auto query_piece = [&](int32_t b, int idx) {
+    const int h = hb * HEADS + idx / (BOXES * 8), piece = idx % (BOXES * 8);
+    return h < G && piece * 8 < a.d ? *reinterpret_cast<const uint4*>(a.q + b * a.q_token + (hq + h) * a.q_head + piece * 16)
+                                    : make_uint4(0, 0, 0, 0);
+  };
+  auto put_piece = [&](int idx, const uint4& v) {
+    const int h = idx / (BOXES * 8), piece = idx % (BOXES * 8), r = h < HW ? h : 32 + h - HW;
+    *reinterpret_cast<uint4*>(smem + (piece >> 3) * kQBlock + r * 128 + (((piece ^ r) & 7) << 4)) = v;
+  };
+  if (warp != kLoadWarp && more && c.s.tiles > 0) {   // the first segment's: everyone, while the first keys come
+    constexpr int kOthers = kThreads - 32;
+    const int t = warp < kLoadWarp ? tid : tid - 32;
+    uint4 v[(kPieces + kOthers - 1) / kOthers];
+#pragma unroll
+    for (int i = 0; i < (kPieces + kOthers - 1) / kOthers; ++i)
+      if (t + i * kOthers < kPieces) v[i] = query_piece(c.b, t + i * kOthers);
+#pragma unroll
+    for (int i = 0; i < (kPieces + kOthers - 1) / kOthers; ++i)
+      if (t + i * kOthers < kPieces) put_piece(t + i * kOthers, v[i]);
+    fence_async_smem_cta();
+    named_barrier_sync(3, kOthers);
+  }
 
   if (warp == kLoadWarp) {
     // ============================================================== keys, values
@@ -194,29 +222,24 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     bool ok = true;
     uint32_t seg = 0;
     for (bool go = more && c.s.tiles > 0; go && ok; ++seg) {
-      // row r of the tile: head r of group 0, r - 32 of group 1, HW of each
-      constexpr int N = HEADS * BOXES * 8 / 32;   // 16-byte pieces per lane
-      uint4 v[N];
+      if (seg > 0) {
+        constexpr int kFlight = 8;   // pieces in flight per lane
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&q_empty), (seg & 1u) ^ 1u));
+        if (!ok) {
+          if (lane == 0) report(a.err, kErrTimeout, x.b, 2);
+          break;
+        }
+#pragma unroll 1
+        for (int i0 = lane; i0 < kPieces; i0 += 32 * kFlight) {
+          uint4 v[kFlight];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int idx = i * 32 + lane, h = idx / (BOXES * 8), piece = idx % (BOXES * 8);
-        const bool in = hb * HEADS + h < G && piece * 8 < a.d;
-        v[i] = in ? *reinterpret_cast<const uint4*>(a.q + x.b * a.q_token + (hq + hb * HEADS + h) * a.q_head + piece * 16)
-                  : make_uint4(0, 0, 0, 0);
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&q_empty), (seg & 1u) ^ 1u));
-      if (!ok) {
-        if (lane == 0) report(a.err, kErrTimeout, x.b, 2);
-        break;
-      }
+          for (int i = 0; i < kFlight; ++i) v[i] = query_piece(x.b, i0 + i * 32);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int idx = i * 32 + lane, h = idx / (BOXES * 8), piece = idx % (BOXES * 8);
-        const int r = h < HW ? h : 32 + h - HW;
-        *reinterpret_cast<uint4*>(smem + (piece >> 3) * kQBlock + r * 128 + (((piece ^ r) & 7) << 4)) = v[i];
+          for (int i = 0; i < kFlight; ++i) put_piece(i0 + i * 32, v[i]);
+        }
+        fence_async_smem_cta();
+        __syncwarp();
       }
-      fence_async_smem_cta();
-      __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&q_full));
       x.tile = x.end;
       go = next_segment<kKeys, kKeys>(a, x);
@@ -331,10 +354,10 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           for (int h = 0; h < HW; ++h) y[h] = -INFINITY;
         }
         if (a.scores != nullptr && key < c.s.n) {
-          float* const sc = a.scores + (bh + h0) * a.score_stride + key;
+          float* sc = a.scores + (bh + h0) * a.score_stride + key;
 #pragma unroll
-          for (int h = 0; h < HW; ++h)
-            if (h0 + h < G) sc[h * a.score_stride] = y[h];
+          for (int h = 0; h < HW; ++h, sc += a.score_stride)
+            if (h0 + h < G) *sc = y[h];
         }
         float over = -INFINITY;
         if (!unset) {
@@ -456,10 +479,14 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             if (a.lse2) a.lse2[bh + h] = nm.lse2;
           }
         }
-        if (lane < HW) s_fac[warp][lane] = whole_unit ? nm.scale : 1.f;
+        if (lane < HW) s_fac[warp][lane] = nm.scale;
       }
       __syncwarp();
       tc::fence_after_sync();
+      const int heads = whole_unit && G - h0 < HW ? G - h0 : HW;   // beyond the group: nothing to write
+      const int dims = whole_unit ? a.d : DP;
+      float* acc = a.part_acc + (piece * HEADS + grp * HW) * DP + row;
+      T* out = reinterpret_cast<T*>(a.out) + (bh + h0) * a.d + row;
 #pragma unroll 1
       for (int i = 0; i < HW / 16; ++i) {
         uint32_t r[16];
@@ -470,14 +497,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
           for (int j = 0; j < 16; ++j) r[j] = 0u;
         }
+        if (row < dims) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int h = 16 * i + j;
-          const float v = __uint_as_float(r[j]) * s_fac[warp][h];
-          if (whole_unit) {
-            if (h0 + h < G && row < a.d) reinterpret_cast<T*>(a.out)[(bh + h0 + h) * a.d + row] = (T)v;
-          } else if (row < DP) {
-            a.part_acc[(piece * HEADS + grp * HW + h) * DP + row] = v;
+          for (int j = 0; j < 16; ++j) {
+            if (16 * i + j < heads) {
+              if (whole_unit) out[(16 * i + j) * (int64_t)a.d] = (T)(__uint_as_float(r[j]) * s_fac[warp][16 * i + j]);
+              else acc[(16 * i + j) * DP] = __uint_as_float(r[j]);
+            }
           }
         }
       }
