@@ -584,6 +584,8 @@ def _kv_scratch(ws, dev, stream, nbytes):
             ws = _kv_ws.get((dev.index, stream))
             if ws is None:
                 ws = _kv_ws[(dev.index, stream)] = Workspace(dev)
+    elif ws.buf is not None and ws.buf.device != dev:
+        raise ValueError(f"the workspace is on {ws.buf.device}, the cache on {dev}")
     return ws.get(nbytes)
 
 

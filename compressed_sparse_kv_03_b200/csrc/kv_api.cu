@@ -257,6 +257,11 @@ csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv
   if (H / kv->n_kv_heads > kMaxGroup)
     return fail(CSA_ERR_UNSUPPORTED, "%s: more than %d query heads per KV head", name, kMaxGroup);
   if ((int64_t)B * H > (1 << 27)) return fail(CSA_ERR_UNSUPPORTED, "%s: too many sequences times heads", name);
+  const char* const q0 = static_cast<const char*>(q->data);
+  const char* const q1 = q0 + 2 * ((B - 1) * q->token_stride + (H - 1) * q->head_stride + kv->head_dim);
+  const char* const o0 = static_cast<const char*>(out);
+  if (q0 < o0 + (int64_t)B * H * kv->head_dim * 2 && o0 < q1)
+    return fail(CSA_ERR_INVALID_ARG, "%s: out must not overlap q", name);
   if (max_len < 0 || max_len > capacity(kv))
     return fail(CSA_ERR_INVALID_ARG, "%s: max_len must be in [0, max_pages*page_size]", name);
   if (window < 0) return fail(CSA_ERR_INVALID_ARG, "%s: window must be >= 0", name);

@@ -59,7 +59,7 @@ struct Shared {
   uint32_t bin, above, count;
   uint32_t few_n;
   uint64_t few[kFew];                 // the cluster's keys of the bin: key, then the lower slot first
-  uint64_t least[WARPS];
+  uint64_t least[WARPS], cta_least;
   uint32_t key_and[4], key_or[4];     // of a pass's candidates
   uint32_t cut;
   int32_t cut_slot;
@@ -354,18 +354,23 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
   };
   int32_t total = 0;
   if (one) {
+    auto warp_least = [](uint64_t x) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const uint64_t x = __shfl_xor_sync(0xffffffffu, least, o);
-      least = x < least ? x : least;
-    }
-    if (lane == 0) s.least[warp] = least;
-    sync();
-    for (int r = 0; r < cs; ++r)
-      for (int w = 0; w < WARPS; ++w) {
-        const uint64_t x = of(&s.least[w], r);
-        least = x < least ? x : least;
+      for (int o = 16; o >= 1; o >>= 1) {
+        const uint64_t y = __shfl_xor_sync(0xffffffffu, x, o);
+        x = y < x ? y : x;
       }
+      return x;
+    };
+    least = warp_least(least);
+    if (lane == 0) s.least[warp] = least;
+    __syncthreads();
+    least = warp_least(lane < WARPS ? s.least[lane] : ~0ull);
+    if (cs > 1) {
+      if (tid == 0) s.cta_least = least;
+      cluster.sync();
+      least = warp_least(lane < cs ? *cluster.map_shared_rank(&s.cta_least, lane) : ~0ull);
+    }
     const int32_t out = (int32_t)~(uint32_t)least;
     total = out < budget;   // the slot above the budget takes its place, or leaves itself
     if (rank == 0 && tid == 0) {

@@ -33,7 +33,7 @@
  *     csa_workspace_check), skips that row and carries on; nothing traps.
  *   - csa_last_error() returns a thread-local description of the last failure.
  *
- * Supported sizes: attention head dim d in {128, 512} (512, the pages' entry
+ * Supported sizes (of the CSA / HCA calls): attention head dim d in {128, 512} (512, the pages' entry
  * width, runs on an mma.sync kernel whose four warps split the dims; the
  * mixed-precision entries and the fused query prologue / output de-rotation
  * need d = 128); indexer key dim c_I in {64, 128}; indexer heads H_I <= 64;
@@ -613,7 +613,10 @@ csa_status_t csa_kv_append(const csa_kv_rows_t* k_new, const csa_kv_rows_t* v_ne
  *                weights_out[b,j,s] = weights[b,j,s] + sum over head j's group
  *                of exp(z - lse) (weights NULL: 0 in its place).  weights may be
  *                weights_out (accumulate in place); slots from lens[b] on are
- *                left as they were.  Needs window == 0; slots >= max_len
+ *                left as they were.  Needs window == 0; slots >= max_len, and
+ *                a workspace of 4 bytes per query head and slot
+ * out must not overlap q.  Groups of more than 16 heads run on tcgen05 (head_dim
+ * up to 128, 16 consecutive slots on one page), all others on mma.sync.
  * Slots on a bad page id are skipped and recorded.  Scores, softmax and output
  * are accumulated in fp32; the probabilities are rounded to the cache's type for
  * the product with the values.

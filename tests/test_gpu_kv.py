@@ -457,6 +457,9 @@ EVICT = [  # B, Hkv, d, lens, page, budget, recent, first, ties
     (1, 2, 64, [5000], 0, 1000, 100, 4, True),
     (1, 1, 256, [9000], 64, 2048, 512, 0, False),
     (9, 8, 64, [65, 64, 80, 1, 0, 70, 66, 79, 67], 16, 64, 16, 4, True),
+    (1, 2, 64, [5001], 0, 5000, 100, 4, True),           # one slot too many, over a cluster
+    (3, 2, 64, [1500, 1501, 1600], 16, 1500, 100, 4, False),
+    (40, 8, 8, [700] * 40, 16, 90, 10, 4, True),         # more moves than are listed in shared memory
 ]
 
 
@@ -485,11 +488,12 @@ def test_evict_matches_oracle(case, layout, inplace):
     assert np.array_equal(f64(cache.k), want[0]) and np.array_equal(f64(cache.v), want[1])
 
 
-@pytest.mark.parametrize("kind", ["zero", "nan", "inf", "negative", "held"])
-def test_evict_of_special_weights(kind):
+@pytest.mark.parametrize("n", [700, 301])
+@pytest.mark.parametrize("kind", ["zero", "nan", "inf", "negative", "held", "tail"])
+def test_evict_of_special_weights(kind, n):
     import compressed_sparse_kv_03_b200 as csa
     g = torch.Generator().manual_seed(25)
-    B, Hkv, n, budget = 2, 2, 700, 300
+    B, Hkv, budget = 2, 2, 300
     cache, table = make_cache(g, B, n, 64, Hkv, 64)
     w, sp, pos = evict_state(g, B, Hkv, n, n, [n, n], budget, 10)
     if kind == "zero":
@@ -503,6 +507,9 @@ def test_evict_of_special_weights(kind):
         w[0, 0, 9] = float("nan")
     elif kind == "negative":
         w.sub_(0.5)
+    elif kind == "tail":     # the newest tokens lie low, the highest slots weigh least
+        sp.copy_(sp.flip(-1))
+        w[:, :, budget:] *= 1e-6
     else:
         sp.fill_(n)      # every slot claims to be recent: the lower ones stay
     dl = torch.tensor([n, n], dtype=torch.int32, device="cuda")

@@ -103,7 +103,8 @@ def test_attention_refuses_bad_arguments_without_launching(lib, mem):
     p = C.c_void_p
     kv, r = cache(base), rows(base)
     # q, kv, lens, B, H, max_len, window, sm_scale, sink, out, lse, weights, weights_out, slots, ws, ws_bytes, stream
-    args = [C.byref(r), C.byref(kv), p(base), 2, 4, 8, 0, 0.1, None, p(base), None, None, None, 0, p(base), 1 << 30, None]
+    out = p(base + 4096)
+    args = [C.byref(r), C.byref(kv), p(base), 2, 4, 8, 0, 0.1, None, out, None, None, None, 0, p(base), 1 << 30, None]
 
     def st(**kw):
         a = list(args)
@@ -117,6 +118,7 @@ def test_attention_refuses_bad_arguments_without_launching(lib, mem):
     assert st(_0=None) == 1
     assert st(_0=C.byref(rows(base, head_stride=4))) == 1
     assert st(_2=None) == 1 and st(_9=None) == 1 and st(_9=p(base + 2)) == 1
+    assert st(_9=p(base)) == 1 and b"overlap" in lib.csa_last_error()
     assert st(_3=-1) == 1 and st(_3=65536) == 2
     assert st(_4=0) == 1 and st(_4=3) == 1 and b"multiple" in lib.csa_last_error()
     assert st(_4=258) == 2 and b"128" in lib.csa_last_error()
