@@ -112,19 +112,24 @@ __device__ __forceinline__ void move_rows(const KvEvictArgs& a, int64_t unit, in
   }
 }
 
-template <int THREADS>
+// CLUSTER: several CTAs per unit (without, all that reaches across them is left
+// out: the kernel runs once through cold code).
+template <int THREADS, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const __grid_constant__ KvEvictArgs a) {
   constexpr int WARPS = THREADS / 32;
   extern __shared__ uint32_t s_keys[];
   __shared__ Shared<WARPS> s;
   cg::cluster_group cluster = cg::this_cluster();
-  const int cs = (int)cluster.num_blocks(), rank = cs == 1 ? 0 : (int)cluster.block_rank();
+  const int cs = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
   auto sync = [&]() {
-    if (cs == 1) __syncthreads();
-    else cluster.sync();
+    if constexpr (CLUSTER) cluster.sync();
+    else __syncthreads();
   };
   // a value of CTA r of the cluster
-  auto of = [&](auto* p, int r) { return cs == 1 ? *p : *cluster.map_shared_rank(p, r); };
+  auto of = [&](auto* p, int r) {
+    if constexpr (CLUSTER) return *cluster.map_shared_rank(p, r);
+    else return *p;
+  };
   const int64_t unit = blockIdx.x / cs;
   const int b = (int)(unit / a.n_kv_heads), h = (int)(unit - (int64_t)b * a.n_kv_heads);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -466,14 +471,14 @@ __global__ void __launch_bounds__(256) kv_evict_lengths_kernel(KvEvictArgs a) {
 
 }  // namespace
 
-template <int THREADS>
+template <int THREADS, bool CLUSTER>
 static cudaError_t launch_threads(const Launch& L, KvEvictArgs& a, int cs) {
   const int64_t units = (int64_t)a.B * a.n_kv_heads;
   const int per = cs * THREADS;   // slots a run advances by
   const int64_t run = ((a.max_len + per / 32 - 1) / (per / 32) + 31) / 32 * 32 * (THREADS / 32);
   a.key_cap = (int32_t)(run <= kMaxCachedKeys ? run : kMaxCachedKeys);
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_shared(kv_evict_kernel<THREADS>, kMaxCachedKeys * (int)sizeof(uint32_t), done);
+  cudaError_t e = allow_shared(kv_evict_kernel<THREADS, CLUSTER>, kMaxCachedKeys * (int)sizeof(uint32_t), done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cs));
@@ -487,7 +492,7 @@ static cudaError_t launch_threads(const Launch& L, KvEvictArgs& a, int cs) {
   cfg.attrs = attr;
   cfg.numAttrs = cs > 1 ? 1 : 0;
   L.begin(kKernelKvEvict);
-  e = cudaLaunchKernelEx(&cfg, kv_evict_kernel<THREADS>, a);
+  e = cudaLaunchKernelEx(&cfg, kv_evict_kernel<THREADS, CLUSTER>, a);
   if (e != cudaSuccess) return e;
   return L.end(kKernelKvEvict);
 }
@@ -501,7 +506,8 @@ cudaError_t launch_kv_evict(const Launch& L, const KvEvictArgs& args) {
   const int64_t units = (int64_t)a.B * a.n_kv_heads;
   int cs = 1;
   while (cs < kMaxCluster && a.max_len > 1024 * cs && (units * cs * 2 <= 296 || a.max_len > (int64_t)kMaxCachedKeys * cs)) cs *= 2;
-  cudaError_t e = units * cs <= 296 ? launch_threads<512>(L, a, cs) : launch_threads<256>(L, a, cs);
+  cudaError_t e = cs > 1 ? launch_threads<512, true>(L, a, cs)
+                  : units <= 296 ? launch_threads<512, false>(L, a, cs) : launch_threads<256, false>(L, a, cs);
   if (e != cudaSuccess) return e;
   if (a.list_len > 0 && (cs > 1 || a.list_len > kSmemList)) {
     const unsigned y = (unsigned)(units < 32768 ? units : 32768);
