@@ -507,7 +507,9 @@ class KVCache:
     contiguous, so head-major storage and interleaved keys and values are
     views), with page_table [n_seq, max_pages] int32, or without one: sequence
     b is page b.  k and v may be one tensor (shared KV).  Holds the tensors;
-    the struct passed to the library is made once."""
+    the struct passed to the library is made once.  What the kernels record
+    (bad lengths or page ids, no room) is read with check() of the Workspace
+    that a call was given."""
 
     def __init__(self, k, v, page_table=None):
         for name, t in (("k", k), ("v", v)):
@@ -650,7 +652,7 @@ def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0,
     """Attention of one token per sequence, q [B, H, d], over slots
     0 .. lens[b]-1 of its sequence (or the last `window` of them); H a multiple
     of the cache's heads, whose groups of query heads share a KV head.  max_len
-    bounds the lengths (default: the cache's capacity).  With weights_out
+    bounds the lengths (default: the cache's capacity, or the weights' slots).  With weights_out
     [B, H_kv, slots] fp32 every slot's probability, summed over the group, is
     added to weights (default: to zero) and stored there; `weights` alone is
     updated in place."""
@@ -659,8 +661,6 @@ def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0,
         raise ValueError(f"{B} sequences, but the cache has {cache.n_seq}")
     qr = _kv_rows(q, "q", cache)
     lp = _kv_array(lens, "lens", torch.int32, B, cache)
-    if max_len is None:
-        max_len = cache.capacity
     slots = 0
     wp = op = None
     if weights is not None and weights_out is None:
@@ -670,6 +670,8 @@ def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0,
         op = _kv_array(weights_out, "weights_out", torch.float32, B, cache, slots)
         if weights is not None:
             wp = _kv_array(weights, "weights", torch.float32, B, cache, slots)
+    if max_len is None:
+        max_len = cache.capacity if op is None else min(cache.capacity, slots)
     if sink is not None:
         _need(sink, "sink", torch.float32, 1, cache.device)
         if sink.shape[0] != H:

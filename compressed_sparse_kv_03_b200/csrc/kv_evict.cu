@@ -142,11 +142,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) kv_evict_kernel(const
   const bool pos_inplace = a.slot_pos_out == a.slot_pos;
 
   if (h == 0 && rank == 0 && tid == 0 && a.lens_out != a.lens) a.lens_out[b] = left;
-  // beyond the old length both arrays are zero
-  for (int64_t j = n + rank * THREADS + tid; j < a.max_len; j += (int64_t)cs * THREADS) {
-    a.weights_out[base + j] = 0.f;
-    a.slot_pos_out[base + j] = 0;
-  }
+  // arrays of their own are zero beyond the old length
+  if (!inplace || !pos_inplace)
+    for (int64_t j = n + rank * THREADS + tid; j < a.max_len; j += (int64_t)cs * THREADS) {
+      if (!inplace) a.weights_out[base + j] = 0.f;
+      if (!pos_inplace) a.slot_pos_out[base + j] = 0;
+    }
   if (a.src_out)
     for (int64_t j = left + rank * THREADS + tid; j < budget; j += (int64_t)cs * THREADS)
       a.src_out[unit * budget + j] = -1;

@@ -647,8 +647,9 @@ csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv
  *   pos                device int32 [B]: position of the newest token
  *   recent >= 1, keep_first >= 0, recent + keep_first <= budget
  *   weights, slot_pos  [B, n_kv_heads, slots], slots >= max_len; the *_out arrays
- *                      may be the same memory (in place) or wholly apart.  They
- *                      are written at 0 .. max_len-1, zeros from lens_out[b] on
+ *                      may be the same memory (in place: nothing from lens[b] on is
+ *                      touched) or wholly apart (written at 0 .. max_len-1); zeros
+ *                      from lens_out[b] on
  *   lens               device int32 [B], lens[b] <= max_len; lens_out may be lens
  *   src_out            int32 [B, n_kv_heads, budget] or NULL: the slot that each
  *                      slot's row came from (itself if it stayed), -1 from

@@ -84,8 +84,9 @@ def kv_weigh(weights, prob, n_kv_heads):
     return out
 
 
-def kv_evict(k, v, table, lens, weights, slot_pos, pos, budget, recent, keep_first=0, max_len=None):
-    """Returns copies (k, v, lens, weights, slot_pos, src)."""
+def kv_evict(k, v, table, lens, weights, slot_pos, pos, budget, recent, keep_first=0, max_len=None, inplace=False):
+    """Returns copies (k, v, lens, weights, slot_pos, src); weights and positions
+    from the old length on are zero, or in place as they were."""
     k, v = k.copy(), v.copy()
     B, heads, slots = weights.shape
     max_len = slots if max_len is None else max_len
@@ -105,8 +106,9 @@ def kv_evict(k, v, table, lens, weights, slot_pos, pos, budget, recent, keep_fir
             came = dict((j, j) for j in stay if j < budget)
             holes = [j for j in range(int(new[b])) if j not in came]
             came.update(zip(holes, [j for j in stay if j >= budget]))
-            w_out[b, h, :max_len] = 0
-            p_out[b, h, :max_len] = 0
+            end = n if inplace else max_len
+            w_out[b, h, :end] = 0
+            p_out[b, h, :end] = 0
             for to, j in came.items():
                 w_out[b, h, to], p_out[b, h, to], src[b, h, to] = weights[b, h, j], slot_pos[b, h, j], j
                 if to != j:

@@ -476,7 +476,7 @@ def test_evict_matches_oracle(case, layout, inplace):
     dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
     ml = cache.capacity
     want = oracle.kv_evict(f64(cache.k), f64(cache.v), None if table is None else table.cpu().numpy(), np.array(lens), f64(w),
-                           sp.cpu().numpy(), pos.tolist(), budget, recent, first, ml)
+                           sp.cpu().numpy(), pos.tolist(), budget, recent, first, ml, inplace)
     wo, so, lo = (w, sp, dl) if inplace else (w.clone(), sp.clone(), torch.empty_like(dl))
     ws = csa.Workspace("cuda")
     n, src = csa.kv_evict(cache, dl, w, sp, pos, budget, recent, keep_first=first, max_len=ml, lens_out=lo, weights_out=wo,
@@ -644,7 +644,7 @@ def test_decode_loop_with_eviction(graph):
         got = f64(w_seen)
         assert np.abs(f64(out) - ro).max() < 2e-2
         assert np.abs(got - want).max() < 1e-4      # 20 steps of at most 4 (2 dz + ..): about 1e-5
-        ok, ov, on, ow, osp, _ = oracle.kv_evict(ok, ov, tb, on, got, osp, at, budget, recent, 2, cap)
+        ok, ov, on, ow, osp, _ = oracle.kv_evict(ok, ov, tb, on, got, osp, at, budget, recent, 2, cap, inplace=True)
         assert lens.tolist() == list(on)
         assert np.array_equal(f64(w), ow) and np.array_equal(sp.cpu().numpy(), osp)
         assert np.array_equal(f64(cache.k), ok) and np.array_equal(f64(cache.v), ov)
@@ -671,6 +671,26 @@ def test_two_streams_and_default_workspaces():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, jobs[i][4]) for o in outs[i])
+
+
+def test_a_captured_first_call():
+    """Kernels whose first launch is captured, without a workspace of their own."""
+    import compressed_sparse_kv_03_b200 as csa
+    g = torch.Generator().manual_seed(32)
+    for G, n in ((3, 900), (30, 1300)):
+        cache, _ = make_cache(g, 2, n, 16, 2, 88, torch.float16)
+        q = torch.randn(2, 2 * G, 88, generator=g).half().cuda()
+        lens = torch.tensor([n, n // 3], dtype=torch.int32, device="cuda")
+        w = torch.zeros(2, 2, n, device="cuda")     # fewer slots than the pages hold
+        torch.cuda.synchronize()
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            out = csa.kv_attn_decode(q, cache, lens, 0.1, weights=w)
+        cg.replay()
+        cg.replay()
+        w2 = torch.zeros_like(w)
+        assert torch.equal(out, csa.kv_attn_decode(q, cache, lens, 0.1, weights=w2))
+        assert torch.allclose(w, 2 * w2)
 
 
 def test_python_argument_checks():
