@@ -4,7 +4,7 @@
 // Work: every seen key and value is read once for the G query heads of its
 // group; 4 G d flops per 4 d bytes, so HBM bounds it for G <= 32 and the
 // mma.sync rate above.  The layout follows from that:
-//   * A unit is (sequence, KV head, block of up to 64 heads of its group).  Its
+//   * A unit is (sequence, KV head, block of up to 64 heads of its group; 32 of wide ones).  Its
 //     slots are cut into tiles, and the tiles of all sequences, one after the
 //     other, into equal runs, whatever the lengths.  A CTA takes one run of one
 //     head (block) and streams through it without draining its copies between
@@ -17,7 +17,7 @@
 //   * Keys are the M side of mma.m16n8k16, 16 a step, heads the N side, 8 or 16
 //     a warp (mma.sync's rate on this chip is an eighth of tcgen05's, so the
 //     columns matter).  Up to 16 heads, the CTA's four warps take the tile's keys apart, each with a ring of its
-//     own (no block barrier in the loop); 32 and 64 heads put 2 and 4 warps
+//     own (no block barrier in the loop); more heads put 2 and 4 warps
 //     side by side on the same keys.  Rows come as TMA boxes of 16 rows (or,
 //     where 16 slots may lie on several pages, by cp.async), page ids one step
 //     ahead of them.
@@ -50,9 +50,9 @@ __device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Resident CTAs per SM: registers (at most 128 a thread with 8 heads a warp, 255
-// with 16) and the ring allow that many.
-constexpr int ctas_per_sm(int dp, int nb) { return dp == 64 ? 4 / nb : dp == 128 ? 2 : 1; }
+// Resident CTAs per SM: registers (at most 128 a thread with 64 dims and 8 heads a
+// warp, 255 otherwise) and the ring allow that many.
+constexpr int ctas_per_sm(int dp, int nb, int wh) { return dp == 64 ? 4 / nb : dp == 128 || wh > 1 ? 2 : 1; }
 
 // NB blocks of 8 heads per warp, WH warps side by side.
 template <class T, int DP, int NB, int WH>
@@ -64,7 +64,7 @@ struct Geometry {
   static constexpr int BOXES = DP / 64;             // 128-byte column blocks of a row
   static constexpr int BOX = kKeys * 128;           // bytes of 16 rows of one
   static constexpr int STAGE = 2 * BOXES * BOX;     // a group's keys, then values
-  static constexpr int CTAS = ctas_per_sm(DP, NB);
+  static constexpr int CTAS = ctas_per_sm(DP, NB, WH);
   static constexpr int STAGES = DP == 64 && CTAS == 2 ? 6 : 3;
   static constexpr int SMEM = STAGES * STAGE * NG + 1024;   // + alignment
   // O of 16 heads fits a stage: joins go through the one that was just read
@@ -515,8 +515,11 @@ cudaError_t launch_typed(const Launch& L, const KvAttnArgs& args, const KvAttnPl
 
 template <class T, int DP>
 cudaError_t launch_wh(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p) {
-  if (p.nb == 1) return launch_typed<T, DP, 1, 1>(L, a, p);
-  return p.wh == 1 ? launch_typed<T, DP, 2, 1>(L, a, p) : p.wh == 2 ? launch_typed<T, DP, 2, 2>(L, a, p) : launch_typed<T, DP, 2, 4>(L, a, p);
+  if (p.nb == 1 && p.wh == 1) return launch_typed<T, DP, 1, 1>(L, a, p);
+  if constexpr (DP <= 128)
+    return p.wh == 1 ? launch_typed<T, DP, 2, 1>(L, a, p) : p.wh == 2 ? launch_typed<T, DP, 2, 2>(L, a, p) : launch_typed<T, DP, 2, 4>(L, a, p);
+  else
+    return p.wh == 2 ? launch_typed<T, DP, 1, 2>(L, a, p) : launch_typed<T, DP, 1, 4>(L, a, p);
 }
 template <class T>
 cudaError_t launch_dp(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p) {
@@ -541,9 +544,14 @@ KvAttnPlan kv_attn_plan(const KvRef& kv, int32_t B, int32_t H, int32_t n_kv_head
   const int G = H / n_kv_heads;
   p.dp = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256;
   p.box_rows = G > 16 && d <= 128 ? kv_attn_tc_box_rows(kv, n_kv_heads) : 0;
-  p.nb = G <= 8 ? 1 : 2;
-  p.wh = G <= 16 ? 1 : G <= 32 ? 2 : 4;
-  p.heads = 8 * p.nb * p.wh;
+  if (p.dp <= 128) {
+    p.nb = G <= 8 ? 1 : 2;
+    p.wh = G <= 16 ? 1 : G <= 32 ? 2 : 4;
+  } else {   // 16 heads of such rows would fill a warp's registers: side by side, and two CTAs an SM
+    p.nb = 1;   // (16 heads of 256 dims on each of 4: 184 -> 97 us)
+    p.wh = G <= 8 ? 1 : G <= 16 ? 2 : 4;
+  }
+  p.heads = p.box_rows ? (G <= 32 ? 32 : 64) : 8 * p.nb * p.wh;
   p.blocks = (G + p.heads - 1) / p.heads;
   p.tile = p.box_rows ? 128 : kKeys * 4 / p.wh;
   const int align = p.box_rows ? 128 : kKeys;   // a window may start that much early, less one
@@ -555,7 +563,7 @@ KvAttnPlan kv_attn_plan(const KvRef& kv, int32_t B, int32_t H, int32_t n_kv_head
   p.max_atoms = (tiles + p.atom - 1) / p.atom;
   p.whole = !invariant && most_slots <= 256;
   const int64_t per_run = (int64_t)n_kv_heads * p.blocks;   // CTAs of a run
-  const int64_t most = (int64_t)kSms * (p.box_rows ? 1 : ctas_per_sm(p.dp, p.nb));
+  const int64_t most = (int64_t)kSms * (p.box_rows ? 1 : ctas_per_sm(p.dp, p.nb, p.wh));
   int64_t runs = most / per_run;
   // many heads may leave a good part of the SMs idle: several waves of shorter runs instead
   if (runs * per_run * 8 < most * 7) runs = (4 * most + per_run - 1) / per_run;

@@ -15,7 +15,7 @@ namespace kvattn {
 constexpr int kFinishThreads = 128;
 constexpr int kSms = 148;
 constexpr int kInvariantSlots = 512;
-constexpr int kMaxBlocks = 2;        // head blocks of a group: up to 128 heads, 64 at a time
+constexpr int kMaxBlocks = 4;        // head blocks of a group: up to 128 heads, 64 (wide ones: 32) at a time
 
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kFinishThreads) kv_finish_kernel(const __grid_
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) ml.x = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, o));
     const float R = ml.x == -INFINITY ? 0.f : ml.x;
-#pragma unroll 8
+#pragma unroll 16
     for (int64_t i = part; i < ps.count; i += split) {
       const int64_t at = ps.at(i) * ROWS + row;
       const float2 p = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
