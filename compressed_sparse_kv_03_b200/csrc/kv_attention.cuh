@@ -15,7 +15,8 @@ namespace kvattn {
 constexpr int kFinishThreads = 128;
 constexpr int kSms = 148;
 constexpr int kInvariantSlots = 512;
-constexpr int kMaxBlocks = 4;        // head blocks of a group: up to 128 heads, 64 (wide ones: 32) at a time
+// Head blocks that a group may have: up to 128 heads, 64 at a time, or 32 wide ones.
+constexpr int max_blocks(int dp, int rows) { return dp > 128 ? (rows == 32 ? 4 : 1) : rows == 64 ? 2 : 1; }
 
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
@@ -204,7 +205,7 @@ constexpr int weigh_slots(int G) { return G <= 16 ? 512 : 128; }
 // the scores, summed over the group in head order.  A lane takes four slots;
 // for up to 16 heads each warp has slots of its own, beyond that the four warps
 // take the heads of the same slots apart and their sums are added in warp order.
-template <int ROWS>
+template <int ROWS, int BLOCKS>
 __device__ void weigh(const KvAttnArgs& a, int b, int kvh, int32_t n, int32_t s0, int32_t end, const Pieces* ps, int blocks) {
   __shared__ float2 s_part[kFinishThreads];
   __shared__ float s_lse[128];
@@ -214,7 +215,9 @@ __device__ void weigh(const KvAttnArgs& a, int b, int kvh, int32_t n, int32_t s0
   const int64_t bh = (int64_t)b * a.H + (int64_t)kvh * G;
   const int row = tid % ROWS, part = tid / ROWS;
   constexpr int PARTS = kFinishThreads / ROWS;
-  for (int hb = 0; hb < blocks; ++hb) {
+#pragma unroll
+  for (int hb = 0; hb < BLOCKS; ++hb) {
+    if (hb >= blocks) break;
     const int h = hb * ROWS + row;
     float2 ml = make_float2(-INFINITY, 0.f);
     if (ps[hb].count > 1) {
@@ -289,14 +292,15 @@ __global__ void __launch_bounds__(kFinishThreads) kv_finish_kernel(const __grid_
   if ((int)blockIdx.x >= join_blocks) {
     const int32_t n = kv_clamp_len(__ldg(a.lens + b), a.max_len, b, nullptr);
     const int32_t s0 = (blockIdx.x - join_blocks) * weigh_per;
-    Pieces ps[kMaxBlocks];
+    constexpr int BLOCKS = max_blocks(DP, ROWS);
+    Pieces ps[BLOCKS];
     if (s0 < n)
 #pragma unroll
-      for (int hb = 0; hb < kMaxBlocks; ++hb)
+      for (int hb = 0; hb < BLOCKS; ++hb)
         ps[hb] = a.whole || hb >= blocks ? Pieces{0, 0, 1, 0} : pieces_of<TILE, ALIGN>(a, b, HZ, kvh * blocks + hb, s_scan);
     pdl_wait();
     pdl_trigger();
-    if (s0 < n) weigh<ROWS>(a, b, kvh, n, s0, s0 + weigh_per, ps, blocks);
+    if (s0 < n) weigh<ROWS, BLOCKS>(a, b, kvh, n, s0, s0 + weigh_per, ps, blocks);
     return;
   }
   const int first = blockIdx.x * (4 / split);   // 4 / split heads, in one head block
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kFinishThreads) kv_finish_kernel(const __grid_
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) ml.x = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, o));
     const float R = ml.x == -INFINITY ? 0.f : ml.x;
-#pragma unroll 16
+#pragma unroll 8
     for (int64_t i = part; i < ps.count; i += split) {
       const int64_t at = ps.at(i) * ROWS + row;
       const float2 p = *reinterpret_cast<const float2*>(a.part_ml + at * 2);

@@ -93,7 +93,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
   constexpr uint32_t kIdescPV = kBf16 ? tc::idesc_bf16(128, kHeads, true, true) : tc::idesc_fp16(128, kHeads, true, true);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kv_full[SLOTS], kv_empty[SLOTS];
-  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], p_empty[2], o_full, o_empty, o_step;
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], p_empty[2], o_full, o_empty;
   __shared__ int64_t s_scan[kThreads / 32], s_first[2];
   __shared__ uint32_t s_tmem;
   __shared__ uint8_t s_rows[kOkRing];            // of a tile: bit i, rows 16 i .. 16 i + 15 lie on a page of the pool
@@ -128,7 +128,6 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     mbar_init(smem_u32(&q_empty), 1);
     mbar_init(smem_u32(&o_full), 1);
     mbar_init(smem_u32(&o_empty), kSmWarps);
-    mbar_init(smem_u32(&o_step), 1);
     mbar_fence_init();
   }
   // the columns of P^T and rows of Q that no head has stay zero
@@ -266,14 +265,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         if (first && !mbar_wait(smem_u32(&o_empty), (seg & 1u) ^ 1u)) return false;
         if (!mbar_wait(smem_u32(&kv_full[slot]), ring_phase(n, SLOTS))) return false;
         tc::fence_after_sync();
-        const uint32_t v = kv_sm + slot * Geo::SLOT, pt = p_sm + pb * kPTile;
+        // 16 keys are 2048 bytes: 128 on in a descriptor's address field
+        const uint64_t v = tc::smem_desc_mn_sw128(kv_sm + slot * Geo::SLOT, kBlock);
+        const uint64_t pt = tc::smem_desc_mn_sw128(p_sm + pb * kPTile, kPTile);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc::mma_bf16_ss(tm_o, tc::smem_desc_mn_sw128(v + kk * 2048, kBlock), tc::smem_desc_mn_sw128(pt + kk * 2048, kPTile),
-                          kIdescPV, !(first && kk == 0));
+        for (int kk = 0; kk < kKeys / 16; ++kk) tc::mma_bf16_ss(tm_o, v + kk * 128, pt + kk * 128, kIdescPV, !(first && kk == 0));
         tc::mma_commit(smem_u32(&kv_empty[slot]));
         tc::mma_commit(smem_u32(&p_empty[pb]));
-        tc::mma_commit(smem_u32(&o_step));
         return true;
       };
       for (bool go = more && c.s.tiles > 0; go && ok; ++seg) {
@@ -288,11 +286,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                mbar_wait(smem_u32(&s_empty[sb]), (uint32_t)(((tile >> 1) & 1) ^ 1));
           if (!ok) break;
           tc::fence_after_sync();
-          const uint32_t k = kv_sm + slot * Geo::SLOT;
+          const uint64_t k = tc::smem_desc_sw128(kv_sm + slot * Geo::SLOT), q = tc::smem_desc_sw128(q_sm);
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk)
-            tc::mma_bf16_ss(tm_s + sb * kHeads, tc::smem_desc_sw128(k + (kk >> 2) * kBlock + (kk & 3) * 32),
-                            tc::smem_desc_sw128(q_sm + (kk >> 2) * kQBlock + (kk & 3) * 32), kIdescS, kk > 0);
+            tc::mma_bf16_ss(tm_s + sb * kHeads, k + ((kk >> 2) * kBlock + (kk & 3) * 32) / 16,
+                            q + ((kk >> 2) * kQBlock + (kk & 3) * 32) / 16, kIdescS, kk > 0);
           tc::mma_commit(smem_u32(&s_full[sb]));
           if (!shared_kv) tc::mma_commit(smem_u32(&kv_empty[slot]));
           if (x.tile + 1 == x.end) tc::mma_commit(smem_u32(&q_empty));
@@ -403,8 +401,9 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
           for (int h = 0; h < HW; ++h) sum[h] *= s_fac[warp][h];
           if (c.tile > first_tile && __any_sync(0xffffffffu, f != 1.f)) {
-            // this warp's dims of O^T; every product so far must be done
-            if (!mbar_wait(smem_u32(&o_step), (uint32_t)((tile - 1) & 1))) fail(5);
+            // this warp's dims of O^T; every product so far must be done (the last
+            // one's P buffer is then free; the one before it was waited for)
+            if (!mbar_wait(smem_u32(&p_empty[sb ^ 1u]), (uint32_t)(((tile - 1) >> 1) & 1))) fail(5);
             __syncwarp();
             tc::fence_after_sync();
 #pragma unroll
