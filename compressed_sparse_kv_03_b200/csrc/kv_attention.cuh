@@ -251,7 +251,7 @@ __device__ void weigh(const KvAttnArgs& a, int b, int kvh, int32_t n, int32_t s0
     for (int i = 0; i < 4; ++i) old[i] = a.weights && i < mine && first + i * 32 < end ? a.weights[at + first + i * 32] : 0.f;
     float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
     if (s < end) {   // a row of scores ends on a multiple of 32
-#pragma unroll 8
+#pragma unroll 4
       for (int h = split ? warp : 0; h < G; h += split ? 4 : 1) {
         const float4 z = *reinterpret_cast<const float4*>(sc + h * a.score_stride);
         const float e = s_lse[h];
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kFinishThreads) kv_finish_kernel(const __grid_
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) ml.x = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, o));
     const float R = ml.x == -INFINITY ? 0.f : ml.x;
-#pragma unroll 8
+#pragma unroll 4
     for (int64_t i = part; i < ps.count; i += split) {
       const int64_t at = ps.at(i) * ROWS + row;
       const float2 p = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
