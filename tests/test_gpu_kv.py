@@ -151,6 +151,8 @@ ATTEND = [
     (4, 8, 2, 128, [80, 0, 1, 200], 3, "interleaved"),
     (70, 8, 2, 64, None, 16, "token"),                   # more sequences than a warp; ragged
     (2, 8, 8, 128, [5000, 40], 64, "token"),             # many CTAs per unit
+    (300, 4, 2, 64, None, 16, "token"),                  # several sequences a thread where runs are cut
+    (200, 20, 1, 64, None, 16, "token"),
 ]
 
 
