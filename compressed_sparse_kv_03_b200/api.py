@@ -93,14 +93,16 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf = None
+        self._at, self._size = None, 0   # the aligned part of buf
 
     def get(self, nbytes):
         nbytes = max(int(nbytes), 256)
-        if self.buf is None or self.buf.numel() < nbytes + 256:
+        if self._size < nbytes:
             self.buf = torch.zeros(nbytes + 256, dtype=torch.uint8, device=self.device)
-        base = self.buf.data_ptr()
-        off = (-base) % 256
-        return C.c_void_p(base + off), self.buf.numel() - off
+            base = self.buf.data_ptr()
+            off = (-base) % 256
+            self._at, self._size = C.c_void_p(base + off), self.buf.numel() - off
+        return self._at, self._size
 
     def check(self, stream=None):
         """Synchronise and raise CsaError if a kernel recorded a device check."""
@@ -539,7 +541,7 @@ class KVCache:
                            None if page_table is None else page_table.data_ptr(), self.max_pages,
                            self.page_size, self.n_kv_heads, self.head_dim, _KV_DTYPES[k.dtype])
         self._ref = C.byref(self._c)
-        self._need = {}   # workspace sizes of the attention calls made so far
+        self._need, self._need_evict = {}, {}   # workspace sizes of recent calls
 
     @staticmethod
     def new(n_seq, max_len, n_kv_heads, head_dim, dtype=torch.bfloat16, device="cuda"):
@@ -552,24 +554,24 @@ class KVCache:
 def _kv_rows(t, name, cache, heads=None):
     if t.dtype is not cache.dtype or t.device != cache.device:
         raise TypeError(f"{name} must be {cache.dtype} on {cache.device}, got {t.dtype} on {t.device}")
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [T, {'H' if heads is None else heads}, {cache.head_dim}], "
-                         f"got {tuple(t.shape)}")
-    n, h, d = t.shape
+                         f"got {tuple(shape)}")
+    n, h, d = shape
     ts, hs, es = t.stride()
     if es != 1 and d > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return C.byref(KvRowsT(t.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0))
 
 
-def _kv_array(t, name, dtype, B, cache, slots=None):
+def _kv_array(t, name, dtype, shape, dev):
     """A [B] or [B, H_kv, slots] array beside the cache; returns its pointer."""
-    shape = (B,) if slots is None else (B, cache.n_kv_heads, slots)
-    if t.dtype is not dtype or t.device != cache.device:
-        raise TypeError(f"{name} must be {dtype} on {cache.device}, got {t.dtype} on {t.device}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype or t.device != dev:
+        raise TypeError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
+    raise ValueError(f"{name} must be contiguous {list(shape)}, got {tuple(t.shape)}")
 
 
 _kv_ws = {}
@@ -586,7 +588,7 @@ def _kv_scratch(ws, dev, stream, nbytes):
             ws = _kv_ws.get((dev.index, stream))
             if ws is None:
                 ws = _kv_ws[(dev.index, stream)] = Workspace(dev)
-    elif ws.buf is not None and ws.buf.device != dev:
+    elif ws.buf is not None and ws.buf.get_device() != dev.index:
         raise ValueError(f"the workspace is on {ws.buf.device}, the cache on {dev}")
     return ws.get(nbytes)
 
@@ -620,10 +622,11 @@ def kv_append(k_new, v_new, cache: KVCache, lens, *, token_start=None, pos=None,
         raise ValueError(f"{B} sequences, but the cache has {cache.n_seq}")
     kr = _kv_rows(k_new, "k_new", cache, cache.n_kv_heads)
     vr = _kv_rows(v_new, "v_new", cache, cache.n_kv_heads)
-    lp = _kv_array(lens, "lens", torch.int32, B, cache)
+    dev, per_seq = cache.device, (B,)
+    lp = _kv_array(lens, "lens", torch.int32, per_seq, dev)
     if lens_out is None:
         lens_out = lens
-    op = _kv_array(lens_out, "lens_out", torch.int32, B, cache)
+    op = lp if lens_out is lens else _kv_array(lens_out, "lens_out", torch.int32, per_seq, dev)
     if token_start is not None:
         _need(token_start, "token_start", torch.int32, 1, cache.device)
         if token_start.shape[0] != B + 1:
@@ -632,12 +635,13 @@ def kv_append(k_new, v_new, cache: KVCache, lens, *, token_start=None, pos=None,
     wp = sp = pp = None
     if weights is not None or slot_pos is not None:
         slots = (weights if weights is not None else slot_pos).shape[-1]
+        per_slot = (B, cache.n_kv_heads, slots)
         if weights is not None:
-            wp = _kv_array(weights, "weights", torch.float32, B, cache, slots)
+            wp = _kv_array(weights, "weights", torch.float32, per_slot, dev)
         if slot_pos is not None:
-            sp = _kv_array(slot_pos, "slot_pos", torch.int32, B, cache, slots)
+            sp = _kv_array(slot_pos, "slot_pos", torch.int32, per_slot, dev)
     if pos is not None:
-        pp = _kv_array(pos, "pos", torch.int32, B, cache)
+        pp = _kv_array(pos, "pos", torch.int32, per_seq, dev)
     tp = None if token_start is None else token_start.data_ptr()
 
     def body(s):
@@ -660,16 +664,18 @@ def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0,
     if B > cache.n_seq:
         raise ValueError(f"{B} sequences, but the cache has {cache.n_seq}")
     qr = _kv_rows(q, "q", cache)
-    lp = _kv_array(lens, "lens", torch.int32, B, cache)
+    dev = cache.device
+    lp = _kv_array(lens, "lens", torch.int32, (B,), dev)
     slots = 0
     wp = op = None
     if weights is not None and weights_out is None:
         weights_out = weights
     if weights_out is not None:
         slots = weights_out.shape[-1]
-        op = _kv_array(weights_out, "weights_out", torch.float32, B, cache, slots)
+        per_slot = (B, cache.n_kv_heads, slots)
+        op = _kv_array(weights_out, "weights_out", torch.float32, per_slot, dev)
         if weights is not None:
-            wp = _kv_array(weights, "weights", torch.float32, B, cache, slots)
+            wp = op if weights is weights_out else _kv_array(weights, "weights", torch.float32, per_slot, dev)
     if max_len is None:
         max_len = cache.capacity if op is None else min(cache.capacity, slots)
     if sink is not None:
@@ -690,6 +696,8 @@ def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0,
         need = cache._need.get(key)
         for again in (True, False):
             if need is None:
+                if len(cache._need) > 256:
+                    cache._need.clear()
                 need = cache._need[key] = lib.csa_kv_attn_decode_workspace_size(B, H, cache._ref, max_len,
                                                                                0 if op is None else 1)
             wsp, wsb = _kv_scratch(ws, cache.device, s, need)
@@ -721,21 +729,27 @@ def kv_evict(cache: KVCache, lens, weights, slot_pos, pos, budget, recent, *, ke
     slot_pos_out = slot_pos if slot_pos_out is None else slot_pos_out
     if max_len is None:
         max_len = min(slots, cache.capacity)
-    args = (_kv_array(lens, "lens", torch.int32, B, cache),
-            _kv_array(lens_out, "lens_out", torch.int32, B, cache),
-            _kv_array(weights, "weights", torch.float32, B, cache, slots),
-            _kv_array(weights_out, "weights_out", torch.float32, B, cache, slots),
-            _kv_array(slot_pos, "slot_pos", torch.int32, B, cache, slots),
-            _kv_array(slot_pos_out, "slot_pos_out", torch.int32, B, cache, slots), slots,
-            _kv_array(pos, "pos", torch.int32, B, cache))
+    dev, per_seq, per_slot = cache.device, (B,), (B, cache.n_kv_heads, slots)
+    args = (_kv_array(lens, "lens", torch.int32, per_seq, dev),
+            _kv_array(lens_out, "lens_out", torch.int32, per_seq, dev),
+            _kv_array(weights, "weights", torch.float32, per_slot, dev),
+            _kv_array(weights_out, "weights_out", torch.float32, per_slot, dev),
+            _kv_array(slot_pos, "slot_pos", torch.int32, per_slot, dev),
+            _kv_array(slot_pos_out, "slot_pos_out", torch.int32, per_slot, dev), slots,
+            _kv_array(pos, "pos", torch.int32, per_seq, dev))
 
     def body(s):
         lib = load()
         src = None
         if return_src:
             src = torch.empty((B, cache.n_kv_heads, max(0, budget)), dtype=torch.int32, device=cache.device)
-        wsp, wsb = _kv_scratch(ws, cache.device, s,
-                               lib.csa_kv_evict_workspace_size(B, cache.n_kv_heads, budget, max_len))
+        key = (B, budget, max_len)
+        need = cache._need_evict.get(key)
+        if need is None:
+            if len(cache._need_evict) > 256:
+                cache._need_evict.clear()
+            need = cache._need_evict[key] = lib.csa_kv_evict_workspace_size(B, cache.n_kv_heads, budget, max_len)
+        wsp, wsb = _kv_scratch(ws, cache.device, s, need)
         check(lib.csa_kv_evict(cache._ref, *args, B, budget, recent, keep_first, max_len, _ptr(src), wsp, wsb, s))
         return (lens_out, src) if return_src else lens_out
     return _kv_run(cache.device, stream, body)
