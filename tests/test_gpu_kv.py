@@ -462,6 +462,7 @@ EVICT = [  # B, Hkv, d, lens, page, budget, recent, first, ties
     (1, 2, 64, [5001], 0, 5000, 100, 4, True),           # one slot too many, over a cluster
     (3, 2, 64, [1500, 1501, 1600], 16, 1500, 100, 4, False),
     (40, 8, 8, [700] * 40, 16, 90, 10, 4, True),         # more moves than are listed in shared memory
+    (2, 2, 64, [50, 64], 16, 100, 10, 4, False),         # a budget above the cache's room
 ]
 
 
@@ -736,6 +737,10 @@ def test_python_argument_checks():
     # nothing to do
     assert csa.kv_attn_decode(q[:0], cache, lens[:0], 0.1).shape == (0, 4, 64)
     assert csa.kv_append(q[:0, :2], q[:0, 2:], cache, lens[:0]).shape == (0,)
+    none = torch.zeros(2, dtype=torch.int32, device="cuda")
+    full = torch.ones(2, 2, 64, device="cuda")
+    assert torch.all(csa.kv_attn_decode(q, cache, none, 0.1, max_len=0, weights=full) == 0) and torch.all(full == 1)
+    assert csa.kv_evict(cache, none.clone(), full, sp, none, 4, 2, max_len=0).tolist() == [0, 0]
     # broadcast heads can be read
     out = csa.kv_attn_decode(q, csa.KVCache(wide, wide, cache.page_table), lens, 0.1)
     assert torch.all(out == 0)
