@@ -4,9 +4,11 @@
 //
 // Work: every seen key and value is read once for the G query heads of its
 // group; 4 G d flops per 4 d bytes, so HBM bounds it for G <= 16 and the
-// mma.sync rate above (8 sequences x 131072 slots, 8 heads of 128: 615 us, 7.0 TB/s
-// with 8 query heads each, the same with 16).  The layout follows from that:
-//   * A unit is (sequence, KV head, block of up to 64 heads of its group; 32 of wide ones).  Its
+// mma.sync rate above (8 sequences x 131072 slots of 128 dims: 8 query heads on
+// each of 8 KV heads 615 us, 16 on each of 4 325 us: 7.0 and 6.6 TB/s).  The
+// layout follows from that:
+//   * A unit is (sequence, KV head, block of up to 64 heads of its group, or 32 of
+//     wide ones).  Its
 //     slots are cut into tiles, and the tiles of all sequences, one after the
 //     other, into equal runs, whatever the lengths.  A CTA takes one run of one
 //     head (block) and streams through it without draining its copies between
@@ -20,9 +22,9 @@
 //     a warp (mma.sync's rate on this chip is an eighth of tcgen05's, so the
 //     columns matter).  Up to 16 heads, the CTA's four warps take the tile's
 //     keys apart, each with a ring of its own (no block barrier in the loop);
-//     more heads put 2 and 4 warps side by side on the same keys.  Rows come as TMA boxes of 16 rows (or,
-//     where 16 slots may lie on several pages, by cp.async), page ids one step
-//     ahead of them.
+//     more heads put 2 and 4 warps side by side on the same keys.  Rows come as
+//     TMA boxes of 16 rows (or, where 16 slots may lie on several pages, by
+//     cp.async), page ids one step ahead of them.
 //   * Softmax with a running maximum in base 2 and fp32; probabilities rounded
 //     to the cache's type for P V (as every 16-bit tensor-core product needs),
 //     their sum taken before that rounding.
