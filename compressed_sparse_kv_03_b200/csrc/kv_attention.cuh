@@ -386,7 +386,9 @@ template <class T, int DP, int TILE, int ALIGN, int ROWS>
 cudaError_t launch_finish(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p) {
   if (p.whole && a.weights_out == nullptr) return cudaSuccess;
   const int G = a.H / a.n_kv_heads;
-  const int split = (int64_t)a.B * a.n_kv_heads * p.blocks * 4 > p.n_ctas ? 1 : 4;   // 4 where a unit has many pieces
+  // warps of a head: 4 where a unit has many pieces.  The order of the sums follows
+  // it, so with fixed slices it is fixed as well
+  const int split = !a.invariant && (int64_t)a.B * a.n_kv_heads * p.blocks * 4 > p.n_ctas ? 1 : 4;
   const int join = p.whole ? 0 : (G * split + 3) / 4;
   // weighing blocks long enough that about eight an SM do it all: each first
   // finds its unit's pieces and sums (32 sequences of up to 8192 slots, 8 heads a group: 26 -> 19 us)

@@ -744,3 +744,36 @@ def test_python_argument_checks():
     # broadcast heads can be read
     out = csa.kv_attn_decode(q, csa.KVCache(wide, wide, cache.page_table), lens, 0.1)
     assert torch.all(out == 0)
+
+
+# ---- promises that hold whatever the batch, the bounds and the free pages --------
+@pytest.mark.parametrize("G", [8, 20, 40])
+def test_batch_invariant_mode_beside_many_sequences_and_other_bounds(G):
+    """A sequence's bits alone, beside 23 others, and under a tighter max_len: the
+    order in which slices are joined follows none of these."""
+    import compressed_sparse_kv_03_b200 as csa
+    g = torch.Generator().manual_seed(33)
+    B, Hkv, d, page, per = 24, 8, 128, 64, 128
+    k, v = (torch.randn(160, page, Hkv, d, generator=g).bfloat16().cuda() for _ in range(2))
+    table = torch.randint(0, 160, (B, per), generator=g, dtype=torch.int32).cuda()   # reading: pages may be shared
+    lens = [3000, 1, 0, 511, 512, 513, 8192] + torch.randint(600, 3000, (B - 7,), generator=g).tolist()
+    q = (2 * torch.randn(B, Hkv * G, d, generator=g)).bfloat16().cuda()
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def run(rows, **kw):
+        w = torch.zeros(len(rows), Hkv, 8192, device="cuda")
+        o, l = csa.kv_attn_decode(q[rows], csa.KVCache(k, v, table[rows]), dl[rows], 0.09, return_lse=True, weights_out=w, **kw)
+        plain = csa.kv_attn_decode(q[rows], csa.KVCache(k, v, table[rows]), dl[rows], 0.09, **kw)
+        assert torch.equal(o, plain)
+        return o, l, w
+
+    csa.set_batch_invariant(True)
+    try:
+        o, l, w = run(list(range(B)))
+        for rows, kw in [([i], {}) for i in range(B)] + [([i], {"max_len": 3000}) for i in (0, 8, 15)] + [
+                (list(range(7, B)), {"max_len": 3000}), ([0, 5, 6, 9], {}), ([23, 0, 7], {"max_len": 3001})]:
+            o1, l1, w1 = run(rows, **kw)
+            for j, i in enumerate(rows):
+                assert torch.equal(o1[j], o[i]) and torch.equal(l1[j], l[i]) and torch.equal(w1[j], w[i]), (i, rows, kw)
+    finally:
+        csa.set_batch_invariant(False)
