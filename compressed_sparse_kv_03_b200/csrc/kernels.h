@@ -457,6 +457,7 @@ struct KvAttnPlan {
   int dp;                       // padded head dim
   int tile;                     // slots of a tile
   int runs, n_ctas, whole, atom;
+  int invariant;                // fixed slices; the layout and the kernels follow this one reading of the switch
   int64_t max_atoms, pieces;    // pieces: partial results that may exist
 };
 KvAttnPlan kv_attn_plan(const KvRef& kv, int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int64_t max_len,

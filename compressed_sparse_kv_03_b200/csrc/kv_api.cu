@@ -307,7 +307,7 @@ csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv
   a.runs = l.plan.runs;
   a.whole = l.plan.whole;
   a.atom = l.plan.atom;
-  a.invariant = batch_invariant();
+  a.invariant = l.plan.invariant;
   a.max_atoms = l.plan.max_atoms;
   a.err = static_cast<WsHeader*>(ws);
   Launch L{(cudaStream_t)stream};

@@ -546,6 +546,7 @@ KvAttnPlan kv_attn_plan(const KvRef& kv, int32_t B, int32_t H, int32_t n_kv_head
                         int32_t window, bool invariant) {
   KvAttnPlan p{};
   const int G = H / n_kv_heads;
+  p.invariant = invariant;
   p.dp = d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256;
   p.box_rows = G > 16 && d <= 128 ? kv_attn_tc_box_rows(kv, n_kv_heads) : 0;
   if (p.dp <= 128) {

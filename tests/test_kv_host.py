@@ -244,3 +244,20 @@ def test_oracle_append_by_hand():
     assert w[:, 0].tolist() == [[1, 0, 0, 0], [0, 1, 1, 1]] and sp[:, 0].tolist() == [[0, 7, 8, 9], [9, 0, 0, 0]]
     # no room: dropped
     assert oracle.kv_append(k, k, table, [3, 0], new, new, [0, 3, 4])[2].tolist() == [4, 1]
+
+
+def test_the_batch_invariant_switch_is_read_once_per_call():
+    """Another thread may change the switch while a call is under way; the workspace
+    layout and the kernel's indexes into it have to follow one reading of it.  (A
+    call that read it twice could write past its workspace, so this is read from
+    the source instead of run.)"""
+    from compressed_sparse_kv_03_b200 import build
+    with open(os.path.join(build.CSRC, "kv_api.cu")) as f:
+        text = f.read()
+    assert text.count("batch_invariant()") == 1
+    body = text[text.index("AttnLayout attn_layout("):]
+    assert "batch_invariant()" in body[:body.index("\n}")]
+    assert "a.invariant = l.plan.invariant;" in text
+    for name in ("kv_attention.cu", "kv_attention.cuh", "kv_attention_tc.cu"):
+        with open(os.path.join(build.CSRC, name)) as f:
+            assert "batch_invariant()" not in f.read()
