@@ -177,11 +177,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const int boxes = kKeys / box_rows;   // row boxes of a tile
     int64_t tile = 0;                     // of the run
     bool ok = true;
-    // lane i < 8: page of the tile's rows 16 i .. 16 i + 15
+    // lane i < 8: page of the tile's rows 16 i .. 16 i + 15; -1 also where nobody
+    // sees any of them (behind the sequence, or before its window: those pages may
+    // be gone)
     int32_t page = -1, row = 0, next_page, next_row;
     auto lookup = [&](const Cursor& x, int32_t& pg, int32_t& rw) {
       const int32_t s = x.s.start + x.tile * kKeys + 16 * lane;
-      pg = lane < 8 && s < x.s.n ? kv_page(a.kv, x.b, s, &rw, a.err) : -1;
+      pg = lane < 8 && s < x.s.n && s + 16 > x.s.lo ? kv_page(a.kv, x.b, s, &rw, a.err) : -1;
     };
     Cursor x = c;
     bool live = more && c.s.tiles > 0;
@@ -204,12 +206,17 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           break;
         }
         const int step = box_rows / 16;
-        uint32_t present = 0;   // boxes on a page of the pool
-        for (int i = 0; i < boxes; ++i) present |= ((mask >> (i * step)) & 1u) << i;
+        const uint32_t whole = (1u << step) - 1u;
+        uint32_t present = 0;   // boxes with seen rows on a page of the pool
+        for (int i = 0; i < boxes; ++i) present |= (uint32_t)(((mask >> (i * step)) & whole) != 0) << i;
         if (lane == 0) mbar_arrive_expect_tx(bar, __popc(present) * BOXES * box_rows * 128);
         __syncwarp();
+        // a box lies on one page: that of its last group looked up, which tells where the box begins there
         const int box = lane % boxes, col = lane / boxes;
-        const int32_t pg = __shfl_sync(0xffffffffu, page, box * step), rw = __shfl_sync(0xffffffffu, row, box * step);
+        const uint32_t groups = (mask >> (box * step)) & whole;
+        const int last = groups ? 31 - __clz(groups) : 0;
+        const int32_t pg = __shfl_sync(0xffffffffu, page, box * step + last);
+        const int32_t rw = __shfl_sync(0xffffffffu, row, box * step + last) - 16 * last;
         if (col < BOXES && ((present >> box) & 1u))
           tc::tma_load_4d(kv_sm + slot * Geo::SLOT + col * kBlock + box * box_rows * 128, u == 0 ? &map_k : &map_v, col * 64, kvh, rw,
                           pg, bar);

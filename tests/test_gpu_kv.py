@@ -777,3 +777,28 @@ def test_batch_invariant_mode_beside_many_sequences_and_other_bounds(G):
                 assert torch.equal(o1[j], o[i]) and torch.equal(l1[j], l[i]) and torch.equal(w1[j], w[i]), (i, rows, kw)
     finally:
         csa.set_batch_invariant(False)
+
+
+@pytest.mark.parametrize("page", [16, 32, 48, 64, 128, 7])
+@pytest.mark.parametrize("G", [8, 20, 40])
+def test_pages_behind_a_window_may_be_gone(G, page):
+    """Page ids of slots that no query sees are never looked up: a sliding window's
+    cache whose older pages were given back has no page error, and the same bits."""
+    import compressed_sparse_kv_03_b200 as csa
+    g = torch.Generator().manual_seed(34)
+    lens = [1000, 517, 130, 300, 0, 129]
+    cache, table = make_cache(g, 6, 1000, page, 2, 64)
+    q = torch.randn(6, 2 * G, 64, generator=g).bfloat16().cuda()
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = csa.Workspace("cuda")
+    for window in (1, 17, 100, 128, 200):
+        want = csa.kv_attn_decode(q, cache, dl, 0.1, window=window, return_lse=True, ws=ws)
+        ws.check()
+        for gone in (-1, cache.k.shape[0], 2 ** 31 - 1):
+            t = table.clone()
+            for b, n in enumerate(lens):
+                t[b, :max(0, n - window) // page] = gone      # pages wholly before the window
+                t[b, -(-n // page):] = gone                   # and behind the sequence
+            got = csa.kv_attn_decode(q, csa.KVCache(cache.k, cache.v, t), dl, 0.1, window=window, return_lse=True, ws=ws)
+            ws.check()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
