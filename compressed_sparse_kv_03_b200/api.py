@@ -24,6 +24,7 @@ or a shared-KV cache with k is v):
 from __future__ import annotations
 
 import ctypes as C
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -88,7 +89,9 @@ class Cache:
 
 class Workspace:
     """Device scratch for the calls that take one; grows on demand.  The
-    header is zeroed at allocation (csa_workspace_init)."""
+    header is zeroed at allocation (csa_workspace_init).  It serves one call
+    after the other: threads, streams and captured graphs that run at the same
+    time need one each."""
 
     def __init__(self, device=None):
         self.device = torch.device(device if device is not None else "cuda")
@@ -574,20 +577,28 @@ def _kv_array(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous {list(shape)}, got {tuple(t.shape)}")
 
 
-_kv_ws = {}
+class _KvScratch(threading.local):
+    """Buffers of one host thread, per device and stream (a cudaStream_t as an int)."""
+
+    def __init__(self):
+        self.of = {}
+
+
+_kv_ws = _KvScratch()
 
 
 def _kv_scratch(ws, dev, stream, nbytes):
-    """Scratch of a call without a workspace of its own: one buffer per device
-    and stream (a cudaStream_t as an int), so that calls on two streams never
-    share one; inside a stream capture a buffer from the capture's own pool."""
+    """Scratch of a call without a workspace of its own: one buffer per host
+    thread, device and stream, so that calls on two streams never share one, nor
+    do two threads whose launches mix on one stream; inside a stream capture a
+    buffer from the capture's own pool."""
     if ws is None:
         if torch.cuda.is_current_stream_capturing():
             ws = Workspace(dev)
         else:
-            ws = _kv_ws.get((dev.index, stream))
+            ws = _kv_ws.of.get((dev.index, stream))
             if ws is None:
-                ws = _kv_ws[(dev.index, stream)] = Workspace(dev)
+                ws = _kv_ws.of[(dev.index, stream)] = Workspace(dev)
     elif ws.buf is not None and ws.buf.get_device() != dev.index:
         raise ValueError(f"the workspace is on {ws.buf.device}, the cache on {dev}")
     return ws.get(nbytes)

@@ -261,3 +261,39 @@ def test_the_batch_invariant_switch_is_read_once_per_call():
     for name in ("kv_attention.cu", "kv_attention.cuh", "kv_attention_tc.cu"):
         with open(os.path.join(build.CSRC, name)) as f:
             assert "batch_invariant()" not in f.read()
+
+
+# ---- the Python calls' scratch, streams and devices ------------------------------
+@pytest.fixture
+def no_capture(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+
+def test_threads_on_one_stream_have_scratch_of_their_own(no_capture):
+    """A call makes several launches over its scratch, and the interpreter runs other
+    threads meanwhile: two threads on one stream must not share it.  (Shown on
+    host memory: shared scratch would let one thread's join or row moves run on
+    another's lists.)"""
+    import threading
+    from compressed_sparse_kv_03_b200 import api
+    host, got, both = torch.device("cpu"), {}, threading.Barrier(2, timeout=30)
+
+    def job(name):
+        at, size = api._kv_scratch(None, host, 7, 1000)
+        both.wait()      # the other thread has its own by now
+        again, _ = api._kv_scratch(None, host, 7, 500)
+        more, big = api._kv_scratch(None, host, 7, 100000)
+        other, _ = api._kv_scratch(None, host, 8, 500)
+        got[name] = (at.value, size, again.value, more.value, big, other.value)
+        both.wait()
+
+    threads = [threading.Thread(target=job, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 2
+    for at, size, again, more, big, other in got.values():
+        assert again == at and size >= 1000 and big >= 100000 and other != more   # `at` is free again by then
+    spans = [(got[i][k], got[i][k] + got[i][k + 1]) for i in range(2) for k in (0, 3)]
+    assert spans[0][0] != spans[2][0] and (spans[1][1] <= spans[3][0] or spans[3][1] <= spans[1][0])
