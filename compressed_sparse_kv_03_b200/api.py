@@ -599,8 +599,11 @@ def _kv_scratch(ws, dev, stream, nbytes):
             ws = _kv_ws.of.get((dev.index, stream))
             if ws is None:
                 ws = _kv_ws.of[(dev.index, stream)] = Workspace(dev)
-    elif ws.buf is not None and ws.buf.get_device() != dev.index:
-        raise ValueError(f"the workspace is on {ws.buf.device}, the cache on {dev}")
+    else:
+        # without an index it will be allocated on the current device, which is the cache's
+        on = ws.device if ws.buf is None else ws.buf.device
+        if on.type != dev.type or (on.index is not None and on.index != dev.index):
+            raise ValueError(f"the workspace is on {on}, the cache on {dev}")
     return ws.get(nbytes)
 
 
@@ -609,6 +612,8 @@ def _kv_run(dev, stream, body):
     device's current stream), so that launches and allocations belong there."""
     if stream is None and torch.cuda.current_device() == dev.index:
         return body(torch._C._cuda_getCurrentRawStream(dev.index))
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {dev}")
     with torch.cuda.device(dev):
         if stream is None:
             return body(torch._C._cuda_getCurrentRawStream(dev.index))

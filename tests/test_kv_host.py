@@ -297,3 +297,26 @@ def test_threads_on_one_stream_have_scratch_of_their_own(no_capture):
         assert again == at and size >= 1000 and big >= 100000 and other != more   # `at` is free again by then
     spans = [(got[i][k], got[i][k] + got[i][k + 1]) for i in range(2) for k in (0, 3)]
     assert spans[0][0] != spans[2][0] and (spans[1][1] <= spans[3][0] or spans[3][1] <= spans[1][0])
+
+
+def test_workspaces_and_streams_of_another_device_are_refused(no_capture):
+    """Before anything is allocated or launched: a workspace without memory yet goes
+    by the device it was made for."""
+    import compressed_sparse_kv_03_b200 as csa
+    from compressed_sparse_kv_03_b200 import api
+    first = torch.device("cuda", 0)
+    for where in ("cuda:1", "cpu", torch.device("cuda", 3)):
+        ws = csa.Workspace(where)
+        with pytest.raises(ValueError, match="workspace is on"):
+            api._kv_scratch(ws, first, 7, 256)
+        assert ws.buf is None
+    ws = csa.Workspace("cpu")
+    ws.get(256)      # and one with memory by that
+    with pytest.raises(ValueError, match="workspace is on"):
+        api._kv_scratch(ws, first, 7, 256)
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 7
+
+    with pytest.raises(ValueError, match="stream is on"):
+        api._kv_run(first, Stream(), lambda s: pytest.fail("ran"))
