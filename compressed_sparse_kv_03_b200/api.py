@@ -97,6 +97,7 @@ class Workspace:
         self.device = torch.device(device if device is not None else "cuda")
         self.buf = None
         self._at, self._size = None, 0   # the aligned part of buf
+        self._home = 0                   # the stream (a cudaStream_t) that buf was allocated on
 
     def get(self, nbytes):
         nbytes = max(int(nbytes), 256)
@@ -105,6 +106,7 @@ class Workspace:
             base = self.buf.data_ptr()
             off = (-base) % 256
             self._at, self._size = C.c_void_p(base + off), self.buf.numel() - off
+            self._home = torch._C._cuda_getCurrentRawStream(self.buf.get_device()) if self.buf.is_cuda else 0
         return self._at, self._size
 
     def check(self, stream=None):
@@ -604,6 +606,11 @@ def _kv_scratch(ws, dev, stream, nbytes):
         on = ws.device if ws.buf is None else ws.buf.device
         if on.type != dev.type or (on.index is not None and on.index != dev.index):
             raise ValueError(f"the workspace is on {on}, the cache on {dev}")
+        got = ws.get(nbytes)
+        if ws._home != stream:
+            # dropped or grown, its memory goes back to the stream it came from: not before this call is done
+            ws.buf.record_stream(torch.cuda.current_stream(dev))
+        return got
     return ws.get(nbytes)
 
 

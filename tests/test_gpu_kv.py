@@ -802,3 +802,34 @@ def test_pages_behind_a_window_may_be_gone(G, page):
             got = csa.kv_attn_decode(q, csa.KVCache(cache.k, cache.v, t), dl, 0.1, window=window, return_lse=True, ws=ws)
             ws.check()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_workspace_used_on_a_second_stream():
+    """Memory of a workspace that a call on another stream still uses does not go to
+    the first stream's next tensor when the workspace is dropped or grows."""
+    import compressed_sparse_kv_03_b200 as csa
+    g = torch.Generator().manual_seed(37)
+    cache, _ = make_cache(g, 2, 4000, 16, 2, 64)
+    q = torch.randn(2, 16, 64, generator=g).bfloat16().cuda()
+    lens = torch.tensor([4000, 99], dtype=torch.int32, device="cuda")
+    w = torch.zeros(2, 2, cache.capacity, device="cuda")
+    want = csa.kv_attn_decode(q, cache, lens, 0.1)
+    for grow in (False, True):
+        a, b = torch.cuda.Stream(), torch.cuda.Stream()
+        ws = csa.Workspace("cuda")
+        csa.kv_attn_decode(q, cache, lens, 0.1, ws=ws, stream=a)
+        torch.cuda.synchronize()
+        at, size = ws.buf.data_ptr(), ws.buf.numel()
+        with torch.cuda.stream(b):
+            torch.cuda._sleep(400000000)      # some 0.2 s
+        out = csa.kv_attn_decode(q, cache, lens, 0.1, ws=ws, stream=b)
+        if grow:
+            csa.kv_attn_decode(q, cache, lens, 0.1, ws=ws, stream=b, weights=w)
+            assert ws.buf.data_ptr() != at
+        else:
+            del ws
+        with torch.cuda.stream(a):
+            other = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert all(t.data_ptr() != at for t in other)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
