@@ -24,6 +24,7 @@ or a shared-KV cache with k is v):
 from __future__ import annotations
 
 import ctypes as C
+import operator
 import threading
 from dataclasses import dataclass
 from typing import Optional
@@ -579,6 +580,14 @@ def _kv_array(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous {list(shape)}, got {tuple(t.shape)}")
 
 
+def _kv_int(x, name, bits=31):
+    """x as an int that a C argument of bits + 1 bits holds (ctypes would keep the low ones)."""
+    x = operator.index(x)
+    if x.bit_length() > bits:
+        raise ValueError(f"{name} is out of range: {x}")
+    return x
+
+
 class _KvScratch(threading.local):
     """Buffers of one host thread, per device and stream (a cudaStream_t as an int)."""
 
@@ -701,6 +710,7 @@ def kv_attn_decode(q, cache: KVCache, lens, sm_scale, *, max_len=None, window=0,
             wp = op if weights is weights_out else _kv_array(weights, "weights", torch.float32, per_slot, dev)
     if max_len is None:
         max_len = cache.capacity if op is None else min(cache.capacity, slots)
+    max_len, window = _kv_int(max_len, "max_len", 63), _kv_int(window, "window")
     if sink is not None:
         _need(sink, "sink", torch.float32, 1, cache.device)
         if sink.shape[0] != H:
@@ -752,6 +762,8 @@ def kv_evict(cache: KVCache, lens, weights, slot_pos, pos, budget, recent, *, ke
     slot_pos_out = slot_pos if slot_pos_out is None else slot_pos_out
     if max_len is None:
         max_len = min(slots, cache.capacity)
+    max_len, budget = _kv_int(max_len, "max_len", 63), _kv_int(budget, "budget")
+    recent, keep_first = _kv_int(recent, "recent"), _kv_int(keep_first, "keep_first")
     dev, per_seq, per_slot = cache.device, (B,), (B, cache.n_kv_heads, slots)
     args = (_kv_array(lens, "lens", torch.int32, per_seq, dev),
             _kv_array(lens_out, "lens_out", torch.int32, per_seq, dev),

@@ -833,3 +833,25 @@ def test_a_workspace_used_on_a_second_stream():
         assert all(t.data_ptr() != at for t in other)
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """An int that does not fit the C argument is refused, not cut to its low bits."""
+    import compressed_sparse_kv_03_b200 as csa
+    g = torch.Generator().manual_seed(36)
+    cache, _ = make_cache(g, 2, 64, 16, 2, 64)
+    lens = torch.tensor([60, 33], dtype=torch.int32, device="cuda")
+    w, sp = torch.rand(2, 2, 64, generator=g).cuda(), torch.arange(64, dtype=torch.int32).expand(2, 2, 64).contiguous().cuda()
+    k0, w0 = cache.k.clone(), w.clone()
+    for kw in (dict(budget=2 ** 32 + 20, recent=4), dict(budget=20, recent=2 ** 32 + 4), dict(budget=20, recent=4, keep_first=2 ** 32),
+               dict(budget=20, recent=4, max_len=2 ** 64 + 64), dict(budget=-2 ** 32 + 20, recent=4)):
+        with pytest.raises(ValueError, match="out of range"):
+            csa.kv_evict(cache, lens, w, sp, lens, **kw)
+    q = torch.randn(2, 4, 64, generator=g).bfloat16().cuda()
+    for kw in (dict(window=2 ** 32 + 4), dict(max_len=2 ** 64 + 4), dict(window=-2 ** 33)):
+        with pytest.raises(ValueError, match="out of range"):
+            csa.kv_attn_decode(q, cache, lens, 0.1, **kw)
+    assert lens.tolist() == [60, 33] and torch.equal(cache.k, k0) and torch.equal(w, w0)
+    # numpy's integers are taken
+    a = csa.kv_attn_decode(q, cache, lens, 0.1, window=np.int64(7), max_len=np.int32(64))
+    assert torch.equal(a, csa.kv_attn_decode(q, cache, lens, 0.1, window=7))
