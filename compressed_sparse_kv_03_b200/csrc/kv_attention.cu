@@ -26,8 +26,8 @@
 //     TMA boxes of 16 rows (or, where 16 slots may lie on several pages, by
 //     cp.async), page ids one step ahead of them.
 //   * Softmax with a running maximum in base 2 and fp32; probabilities rounded
-//     to the cache's type for P V (as every 16-bit tensor-core product needs),
-//     their sum taken before that rounding.
+//     to the cache's type for P V (as every 16-bit tensor-core product needs; in
+//     fp16 times 2^14), their sum taken before that rounding.
 #include "kv_attention.cuh"
 
 namespace csa {
@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kThreads, (Geometry<T, DP, NB, WH>::CTAS))
 kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                const __grid_constant__ KvAttnArgs a) {
   using Geo = Geometry<T, DP, NB, WH>;
+  constexpr int LIFT = lift<T>(0);   // scores are at most the running maximum
   constexpr int NG = Geo::NG, TILE = Geo::TILE, S = Geo::STAGES, BOX = Geo::BOX, BOXES = Geo::BOXES, HEADS = Geo::HEADS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // the swizzle's atoms are 1024 bytes
@@ -318,8 +319,8 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const float r0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], r1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
-        const float p0 = ex2(s[nb][0][0] - r0), p1 = ex2(s[nb][0][1] - r1);
-        const float p2 = ex2(s[nb][0][2] - r0), p3 = ex2(s[nb][0][3] - r1);
+        const float p0 = lifted<LIFT>(s[nb][0][0] - r0), p1 = lifted<LIFT>(s[nb][0][1] - r1);
+        const float p2 = lifted<LIFT>(s[nb][0][2] - r0), p3 = lifted<LIFT>(s[nb][0][3] - r1);
         l[nb][0] += p0 + p2;
         l[nb][1] += p1 + p3;
         // (key, 2 heads) to (head, 2 keys)
@@ -345,6 +346,18 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) l[nb][e] += __shfl_xor_sync(0xffffffffu, l[nb][e], off);
+    if constexpr (LIFT > 0) {
+      constexpr float DROP = 1.f / (1 << LIFT);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        l[nb][0] *= DROP;
+        l[nb][1] *= DROP;
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nb][i][j] *= DROP;
+      }
+    }
     const bool whole_unit = first_tile == 0 && c.tile == c.s.tiles;   // no other piece exists
     const int64_t piece = a.invariant ? ((int64_t)c.b * HZ + hz) * a.max_atoms + first_tile / a.atom
                                       : 2 * (int64_t)blockIdx.x + (continued ? 0 : 1);

@@ -30,6 +30,14 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// fp16 ends at 2^-14 (2^-24 with fewer bits), and the probabilities of a long cache
+// can lie below that and still make the output together; they are rounded to the
+// type as p * 2^LIFT, with sums and O on that scale until the segment's end (powers
+// of two: exact).  `top` is log2 of the largest p that occurs; fp16 holds 2^15.
+// bf16 has the exponents of fp32 and needs none.
+template <class T>
+constexpr int lift(int top) { return __is_same(T, __half) ? (top > 0 ? 15 - top : 14) : 0; }
+
 // Slots that a query sees: [lo, n); tiles start at lo rounded down to ALIGN, so
 // that ALIGN slots from there lie on one page wherever page_size is a multiple of it.
 struct Span {
@@ -149,6 +157,13 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
+}
+
+// p * 2^LIFT of log2 p
+template <int LIFT>
+__device__ __forceinline__ float lifted(float x) {
+  if constexpr (LIFT == 0) return ex2(x);
+  return ex2(x + (float)LIFT);
 }
 
 // Final scale and log-sum-exp (base 2) of a head from its maximum and sum.

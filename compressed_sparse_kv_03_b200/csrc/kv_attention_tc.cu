@@ -18,7 +18,7 @@
 //              as they stand; only when some key exceeds its head's by more than
 //              2^8 (a vote of the group, one barrier) are the maxima taken anew
 //              (redux), and O^T and the sums rescaled.  P^T goes to shared memory
-//              in the cache's type.  At the end of a segment thread = dim of O^T.
+//              in the cache's type (fp16: times 2^7).  At the end of a segment thread = dim of O^T.
 //   warp 8     TMEM, tcgen05.mma issue by one thread
 //   warp 9     page ids and TMA
 //   warp 10    the next segment's query heads, into the swizzled tile
@@ -88,6 +88,8 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                   const __grid_constant__ KvAttnArgs a, int box_rows, int shared_kv) {
   using Geo = TcGeometry<DP>;
   constexpr int SLOTS = Geo::SLOTS, BOXES = Geo::BOXES, HEADS = 2 * HW;
+  constexpr int LIFT = lift<T>((int)kGrow);
+  constexpr float DROP = 1.f / (1 << LIFT);
   constexpr bool kBf16 = sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
   constexpr uint32_t kIdescS = kBf16 ? tc::idesc_bf16(128, kHeads) : tc::idesc_fp16(128, kHeads);
   constexpr uint32_t kIdescPV = kBf16 ? tc::idesc_bf16(128, kHeads, true, true) : tc::idesc_fp16(128, kHeads, true, true);
@@ -437,7 +439,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int h = 8 * i + 2 * j;
-            const float p0 = ex2(y[h] + off[2 * j]), p1 = ex2(y[h + 1] + off[2 * j + 1]);
+            const float p0 = lifted<LIFT>(y[h] + off[2 * j]), p1 = lifted<LIFT>(y[h + 1] + off[2 * j + 1]);
             sum[h] += p0;
             sum[h + 1] += p1;
             pk[j] = pack2<T>(p0, p1);
@@ -471,7 +473,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         }
       }
       for (int o = HW; o < 32; o <<= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-      if (lane < HW) s_sum[warp][lane] = sum[0];
+      if (lane < HW) s_sum[warp][lane] = sum[0] * DROP;
       const bool any = c.end > first_tile;   // false: an empty sequence with a CTA to itself
       if (any && !mbar_wait(smem_u32(&o_full), seg & 1u)) fail(8);
       group_any(bar, false);
@@ -491,7 +493,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             if (a.lse2) a.lse2[bh + h] = nm.lse2;
           }
         }
-        if (lane < HW) s_fac[warp][lane] = nm.scale;
+        if (lane < HW) s_fac[warp][lane] = nm.scale * DROP;
       }
       __syncwarp();
       tc::fence_after_sync();
@@ -514,7 +516,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           for (int j = 0; j < 16; ++j) {
             if (16 * i + j < heads) {
               if (whole_unit) out[(16 * i + j) * (int64_t)a.d] = (T)(__uint_as_float(r[j]) * s_fac[warp][16 * i + j]);
-              else acc[(16 * i + j) * DP] = __uint_as_float(r[j]);
+              else acc[(16 * i + j) * DP] = __uint_as_float(r[j]) * DROP;
             }
           }
         }

@@ -621,7 +621,8 @@ csa_status_t csa_kv_append(const csa_kv_rows_t* k_new, const csa_kv_rows_t* v_ne
  * up to 128, 16 consecutive slots on one page), all others on mma.sync.
  * Slots on a bad page id are skipped and recorded.  Scores, softmax and output
  * are accumulated in fp32; the probabilities are rounded to the cache's type for
- * the product with the values.
+ * the product with the values (fp16: times 2^14, or 2^7 on tcgen05, so that those
+ * of a long cache's many small slots are not lost).
  */
 size_t csa_kv_attn_decode_workspace_size(int32_t B, int32_t H, const csa_kv_cache_t* kv,
                                          int64_t max_len, int32_t with_weights);

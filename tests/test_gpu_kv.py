@@ -855,3 +855,37 @@ def test_sizes_beyond_32_bits_are_refused():
     # numpy's integers are taken
     a = csa.kv_attn_decode(q, cache, lens, 0.1, window=np.int64(7), max_len=np.int32(64))
     assert torch.equal(a, csa.kv_attn_decode(q, cache, lens, 0.1, window=7))
+
+
+@pytest.mark.parametrize("G", [8, 12, 40])
+@pytest.mark.parametrize("page", [64, 7])
+def test_many_small_probabilities_in_fp16(G, page):
+    """Four slots 18 nats above 19996 others, whose probabilities (2^-26 of the
+    largest) lie below fp16's subnormals and together make the whole output.
+
+    Maxima belong to a run of slots and, up to 16 heads, to a warp that sees 16 of
+    every 64, so enough sequences are given that a run holds whole ones, and the
+    four slots are 16 apart.  With S = 19996 exp(-18) the output is 16 S / (4 + S).
+    On mma.sync the probabilities are scaled by 2^14 and normal numbers, off by u
+    relative; on tcgen05 by 2^7 and subnormal, off by at most 2^-25 / 2^7 each.  The
+    rest: one rounding of the output, u, and the fp32 exponent, sums and quotient, a
+    few dozen roundings and one per summand (E each)."""
+    import compressed_sparse_kv_03_b200 as csa
+    g = torch.Generator().manual_seed(35)
+    n, d, B, Hkv = 20000, 64, 40, 8
+    cache, table = make_cache(g, 1, n, page, Hkv, d, torch.float16)
+    cache.k.zero_(), cache.v.fill_(16.0)
+    for s in (0, 16, 32, 48):
+        at = (table[0, s // page].long(), s % page)
+        cache.k[at] = torch.tensor([18.0] + [0.0] * (d - 1)).half().cuda()
+        cache.v[at] = 0.0
+    cache = csa.KVCache(cache.k, cache.v, table.expand(B, -1).contiguous())
+    q = torch.zeros(B, Hkv * G, d, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 1.0
+    out, lse = csa.kv_attn_decode(q, cache, torch.full((B,), n, dtype=torch.int32, device="cuda"), 1.0, return_lse=True)
+    s = (n - 4) * math.exp(-18.0)
+    want, u = 16 * s / (4 + s), 2.0 ** -11
+    each = 0.0 if G <= 16 or page == 7 else 2.0 ** -32
+    tol = want * (2 * u + (n + 64) * E) + (n - 4) * each * 16 / 4
+    assert np.abs(f64(out) - want).max() <= tol, (np.abs(f64(out) - want).max(), want, tol)
+    assert np.abs(f64(lse) - (18 + math.log(4 + s))).max() <= (n + 16) * E
