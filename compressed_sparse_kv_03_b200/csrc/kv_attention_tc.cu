@@ -176,7 +176,9 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 
   if (warp == kLoadWarp) {
     // ============================================================== keys, values
-    const int boxes = kKeys / box_rows;   // row boxes of a tile
+    const int boxes = kKeys / box_rows, step = box_rows / 16;   // row boxes of a tile, groups of 16 rows of a box
+    const int box = lane % boxes, col = lane / boxes;           // what this lane copies
+    const uint32_t whole = (1u << step) - 1u;
     int64_t tile = 0;                     // of the run
     bool ok = true;
     // lane i < 8: page of the tile's rows 16 i .. 16 i + 15; -1 also where nobody
@@ -198,6 +200,14 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
       if (live) lookup(x, next_page, next_row);
       const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
       if (lane == 0) s_rows[tile % kOkRing] = (uint8_t)mask;   // released by the arrivals below
+      // a box with seen rows on a page of the pool lies on that page whole; its last
+      // group looked up tells where it begins there
+      const uint32_t groups = (mask >> (box * step)) & whole;
+      const bool present = col < BOXES && groups != 0;
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, present)) * box_rows * 128;
+      const int last = groups ? 31 - __clz(groups) : 0;
+      const int32_t pg = __shfl_sync(0xffffffffu, page, box * step + last);
+      const int32_t rw = __shfl_sync(0xffffffffu, row, box * step + last) - 16 * last;
       for (int u = 0; u < uses; ++u) {
         const int64_t n = tile * uses + u;
         const uint32_t slot = ring_slot(n, SLOTS), bar = smem_u32(&kv_full[slot]);
@@ -207,19 +217,9 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
           ok = false;
           break;
         }
-        const int step = box_rows / 16;
-        const uint32_t whole = (1u << step) - 1u;
-        uint32_t present = 0;   // boxes with seen rows on a page of the pool
-        for (int i = 0; i < boxes; ++i) present |= (uint32_t)(((mask >> (i * step)) & whole) != 0) << i;
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(present) * BOXES * box_rows * 128);
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         __syncwarp();
-        // a box lies on one page: that of its last group looked up, which tells where the box begins there
-        const int box = lane % boxes, col = lane / boxes;
-        const uint32_t groups = (mask >> (box * step)) & whole;
-        const int last = groups ? 31 - __clz(groups) : 0;
-        const int32_t pg = __shfl_sync(0xffffffffu, page, box * step + last);
-        const int32_t rw = __shfl_sync(0xffffffffu, row, box * step + last) - 16 * last;
-        if (col < BOXES && ((present >> box) & 1u))
+        if (present)
           tc::tma_load_4d(kv_sm + slot * Geo::SLOT + col * kBlock + box * box_rows * 128, u == 0 ? &map_k : &map_v, col * 64, kvh, rw,
                           pg, bar);
       }
