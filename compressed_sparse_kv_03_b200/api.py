@@ -99,6 +99,7 @@ class Workspace:
         self.buf = None
         self._at, self._size = None, 0   # the aligned part of buf
         self._home = 0                   # the stream (a cudaStream_t) that buf was allocated on
+        self._dev = -1                   # and its device's index
 
     def get(self, nbytes):
         nbytes = max(int(nbytes), 256)
@@ -107,7 +108,8 @@ class Workspace:
             base = self.buf.data_ptr()
             off = (-base) % 256
             self._at, self._size = C.c_void_p(base + off), self.buf.numel() - off
-            self._home = torch._C._cuda_getCurrentRawStream(self.buf.get_device()) if self.buf.is_cuda else 0
+            self._dev = self.buf.get_device()
+            self._home = torch._C._cuda_getCurrentRawStream(self._dev) if self._dev >= 0 else 0
         return self._at, self._size
 
     def check(self, stream=None):
@@ -582,6 +584,8 @@ def _kv_array(t, name, dtype, shape, dev):
 
 def _kv_int(x, name, bits=31):
     """x as an int that a C argument of bits + 1 bits holds (ctypes would keep the low ones)."""
+    if type(x) is int and 0 <= x < 0x80000000:
+        return x
     x = operator.index(x)
     if x.bit_length() > bits:
         raise ValueError(f"{name} is out of range: {x}")
@@ -611,10 +615,11 @@ def _kv_scratch(ws, dev, stream, nbytes):
             if ws is None:
                 ws = _kv_ws.of[(dev.index, stream)] = Workspace(dev)
     else:
-        # without an index it will be allocated on the current device, which is the cache's
-        on = ws.device if ws.buf is None else ws.buf.device
-        if on.type != dev.type or (on.index is not None and on.index != dev.index):
-            raise ValueError(f"the workspace is on {on}, the cache on {dev}")
+        if ws._dev != dev.index:
+            # without an index it will be allocated on the current device, which is the cache's
+            on = ws.device if ws.buf is None else ws.buf.device
+            if on.type != dev.type or (on.index is not None and on.index != dev.index):
+                raise ValueError(f"the workspace is on {on}, the cache on {dev}")
         got = ws.get(nbytes)
         if ws._home != stream:
             # dropped or grown, its memory goes back to the stream it came from: not before this call is done
