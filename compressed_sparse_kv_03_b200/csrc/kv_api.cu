@@ -102,10 +102,14 @@ csa_status_t check_rows(const csa_kv_rows_t* r, const char* what, const char* na
   return CSA_OK;
 }
 
+bool apart(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
+  return x + a_bytes <= y || y + b_bytes <= x;
+}
+
 // Output arrays are the input's memory or wholly apart from it.
 bool same_or_apart(const void* a, const void* b, int64_t bytes) {
-  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
-  return x == y || x + bytes <= y || y + bytes <= x;
+  return a == b || apart(a, bytes, b, bytes);
 }
 
 KvRef to_ref(const csa_kv_cache_t* kv) {
@@ -197,6 +201,15 @@ csa_status_t csa_kv_append(const csa_kv_rows_t* k_new, const csa_kv_rows_t* v_ne
     return fail(CSA_ERR_INVALID_ARG, "%s: lens_out must be lens or apart from it", name);
   if (slot_pos != nullptr && pos == nullptr)
     return fail(CSA_ERR_INVALID_ARG, "%s: slot_pos needs pos", name);
+  // Blocks write new lengths while others still read pos and token_start; lengths in
+  // place are written by a launch of their own, except with one token per sequence,
+  // where one block reads and writes all of a sequence's.
+  const int64_t n4 = (int64_t)B * 4;
+  if (token_start != nullptr && !apart(lens_out, n4, token_start, n4 + 4))
+    return fail(CSA_ERR_INVALID_ARG, "%s: lens_out must be apart from token_start", name);
+  if (slot_pos != nullptr && (token_start == nullptr ? !same_or_apart(pos, lens_out, n4)
+                                                     : lens_out != lens && !apart(pos, n4, lens_out, n4)))
+    return fail(CSA_ERR_INVALID_ARG, "%s: lens_out must be apart from pos", name);
   if ((weights != nullptr || slot_pos != nullptr) && slots < 1)
     return fail(CSA_ERR_INVALID_ARG, "%s: weights and slot_pos need slots >= 1", name);
   const int64_t pieces = (int64_t)kv->head_dim / 8 * kv->n_kv_heads * 2;
@@ -347,6 +360,8 @@ csa_status_t csa_kv_evict(const csa_kv_cache_t* kv, const int32_t* lens, int32_t
   if (!same_or_apart(lens, lens_out, (int64_t)B * 4) || !same_or_apart(weights, weights_out, bytes) ||
       !same_or_apart(slot_pos, slot_pos_out, bytes))
     return fail(CSA_ERR_INVALID_ARG, "%s: an output must be its input or apart from it", name);
+  if (lens_out != lens && !apart(lens_out, (int64_t)B * 4, pos, (int64_t)B * 4))   // other blocks still read it
+    return fail(CSA_ERR_INVALID_ARG, "%s: lens_out must be lens or apart from pos", name);
   const bool shared = kv->k == kv->v;
   if (shared && (kv->k_page_stride != kv->v_page_stride || kv->k_slot_stride != kv->v_slot_stride ||
                  kv->k_head_stride != kv->v_head_stride))

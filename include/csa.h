@@ -577,7 +577,8 @@ typedef struct {
  *   token_start   device int32 [B+1], ascending: sequence b's tokens are rows
  *                 token_start[b] .. token_start[b+1]-1.  NULL: one token per
  *                 sequence (n_tokens == B)
- *   lens          device int32 [B]; lens_out [B] may be lens (in place)
+ *   lens          device int32 [B]; lens_out [B] may be lens (in place), and is
+ *                 otherwise apart from lens, pos and token_start
  *   weights       fp32 [B, n_kv_heads, slots], or NULL: set to 0 at the new slots
  *   slot_pos      int32 [B, n_kv_heads, slots], or NULL: set to pos[b] + i there
  *   pos           device int32 [B], required with slot_pos: position in the
@@ -653,7 +654,8 @@ csa_status_t csa_kv_attn_decode(const csa_kv_rows_t* q, const csa_kv_cache_t* kv
  *                      may be the same memory (in place: nothing from lens[b] on is
  *                      touched) or wholly apart (written at 0 .. max_len-1); zeros
  *                      from lens_out[b] on
- *   lens               device int32 [B], lens[b] <= max_len; lens_out may be lens
+ *   lens               device int32 [B], lens[b] <= max_len; lens_out may be lens,
+ *                      and is otherwise apart from lens and pos
  *   src_out            int32 [B, n_kv_heads, budget] or NULL: the slot that each
  *                      slot's row came from (itself if it stayed), -1 from
  *                      lens_out[b] on; for arrays kept beside the cache

@@ -320,3 +320,42 @@ def test_workspaces_and_streams_of_another_device_are_refused(no_capture):
 
     with pytest.raises(ValueError, match="stream is on"):
         api._kv_run(first, Stream(), lambda s: pytest.fail("ran"))
+
+
+# ---- arrays that one call both reads and writes ----------------------------------
+def test_new_lengths_do_not_share_memory_with_what_the_call_still_reads(lib, mem):
+    """Blocks write lens_out while others read pos and token_start (host checks: nothing
+    is launched, workspaces that are too small stop the calls that pass)."""
+    _, base = mem
+    before = lib.csa_launch_count()
+    p = C.c_void_p
+    kv, r = cache(base), rows(base)
+    at = {"lens": base, "out": base + 64, "pos": base + 128, "start": base + 192}
+
+    def append(start=None, n=2, pos=at["pos"], lens=at["lens"], out=at["out"], slot_pos=base + 2048):
+        return lib.csa_kv_append(C.byref(r), C.byref(r), C.byref(kv), start and p(start), n, 2, p(lens), p(out), p(pos),
+                                 p(base + 1024), slot_pos and p(slot_pos), 8, p(base), 128, None)
+
+    ws = 5   # what a call that passes the checks before it gives
+    assert append() == ws and append(at["start"], 5) == ws
+    assert append(at["start"], 5, out=at["pos"]) == 1 and b"pos" in lib.csa_last_error()
+    assert append(at["start"], 5, out=at["pos"] + 4) == 1
+    assert append(at["start"], 5, out=at["start"]) == 1 and b"token_start" in lib.csa_last_error()
+    assert append(at["start"], 5, out=at["start"] + 8) == 1      # its last entry
+    assert append(at["start"], 5, out=at["start"] + 12) == ws
+    assert append(out=at["pos"] + 4) == 1                        # another sequence's position
+    assert append(out=at["pos"]) == ws                           # one block reads and writes a sequence's
+    assert append(at["start"], 5, out=at["pos"], slot_pos=None) == ws   # pos is not read
+    # in place the lengths are written when everything has been read
+    assert append(at["start"], 5, out=at["lens"], pos=at["lens"]) == ws
+    assert append(at["start"], 5, lens=at["start"], out=at["start"]) == 1
+
+    def evict(pos=at["pos"], lens=at["lens"], out=at["out"]):
+        return lib.csa_kv_evict(C.byref(kv), p(lens), p(out), p(base + 1024), p(base + 1024), p(base + 2048), p(base + 2048), 8, p(pos),
+                                2, 6, 2, 1, 8, None, p(base), 128, None)
+
+    assert evict() == ws
+    assert evict(out=at["pos"]) == 1 and b"pos" in lib.csa_last_error()
+    assert evict(out=at["pos"] - 4) == 1
+    assert evict(out=at["lens"], pos=at["lens"]) == ws
+    assert lib.csa_launch_count() == before
