@@ -159,11 +159,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// p * 2^LIFT of log2 p
+// p * 2^LIFT of log2 p (multiplied, not added to the exponent, whose bits it would cost)
 template <int LIFT>
 __device__ __forceinline__ float lifted(float x) {
-  if constexpr (LIFT == 0) return ex2(x);
-  return ex2(x + (float)LIFT);
+  return ex2(x) * (float)(1 << LIFT);
 }
 
 // Final scale and log-sum-exp (base 2) of a head from its maximum and sum.
