@@ -889,3 +889,43 @@ def test_many_small_probabilities_in_fp16(G, page):
     tol = want * (2 * u + (n + 64) * E) + (n - 4) * each * 16 / 4
     assert np.abs(f64(out) - want).max() <= tol, (np.abs(f64(out) - want).max(), want, tol)
     assert np.abs(f64(lse) - (18 + math.log(4 + s))).max() <= (n + 16) * E
+
+
+def test_two_threads_on_one_stream_with_default_workspaces():
+    """Calls of two host threads on the default stream, without workspaces: launches of
+    one may come between those of the other."""
+    import threading
+    import compressed_sparse_kv_03_b200 as csa
+    g = torch.Generator().manual_seed(38)
+    jobs, errors = [], []
+    for n, G in ((5000, 4), (7000, 20)):
+        cache, _ = make_cache(g, 3, n, 16, 2, 64)
+        q = torch.randn(3, 2 * G, 64, generator=g).bfloat16().cuda()
+        lens = torch.tensor([n, n // 3, 5], dtype=torch.int32, device="cuda")
+        w, sp, pos = evict_state(g, 3, 2, n, cache.capacity, [n, n // 3, 5], 1000, 100)
+        k0, v0 = cache.k.clone(), cache.v.clone()
+
+        def step(cache=cache, q=q, lens=lens, w=w, sp=sp, pos=pos, k0=k0, v0=v0):
+            wo, so, lo = torch.zeros_like(w), torch.zeros_like(sp), torch.empty_like(lens)
+            cache.k.copy_(k0), cache.v.copy_(v0)
+            out = csa.kv_attn_decode(q, cache, lens, 0.1, weights=w, weights_out=wo)
+            csa.kv_evict(cache, lens, wo, sp, pos, 1000, 100, lens_out=lo, weights_out=wo, slot_pos_out=so)
+            return [out, wo, so, lo, cache.k.clone(), cache.v.clone()]
+        jobs.append((step, step()))
+    torch.cuda.synchronize()
+
+    def run(step, want):
+        try:
+            for got in [step() for _ in range(40)]:
+                assert all(torch.equal(x, y) for x, y in zip(got, want))
+        except BaseException as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    if errors:
+        raise errors[0]
