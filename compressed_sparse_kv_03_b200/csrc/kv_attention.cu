@@ -20,9 +20,10 @@
 //     72 dims read 1.77 times their bytes from HBM.
 //   * Keys are the M side of mma.m16n8k16, 16 a step, heads the N side, 8 or 16
 //     a warp (mma.sync's rate on this chip is an eighth of tcgen05's, so the
-//     columns matter).  Up to 16 heads, the CTA's four warps take the tile's
-//     keys apart, each with a ring of its own (no block barrier in the loop);
-//     more heads put 2 and 4 warps side by side on the same keys.  Rows come as
+//     columns matter).  Up to 16 heads (8 of more than 128 dims), the CTA's four
+//     warps take the tile's keys apart, each with a ring of its own (no block
+//     barrier in the loop); more heads put 2 and 4 warps side by side on the
+//     same keys.  Rows come as
 //     TMA boxes of 16 rows (or, where 16 slots may lie on several pages, by
 //     cp.async), page ids one step ahead of them.
 //   * Softmax with a running maximum in base 2 and fp32; probabilities rounded
@@ -553,8 +554,8 @@ cudaError_t launch_dp(const Launch& L, const KvAttnArgs& a, const KvAttnPlan& p)
 // Which kernel, and how the work is cut.  Groups of more than 16 heads go to the
 // tcgen05 kernel, except at head dims above 128 (its ring and TMEM are laid out
 // for 64 and 128) and on pages that no 16-row box fits: 64 heads on one KV head,
-// 8 x 131072 slots of 128 dims, 130 us there and 270 us here; 32 heads on each of
-// two, 193 and 264 us; 17 heads on one, 111 and 132 us.
+// 8 x 131072 slots of 128 dims, 107 us there and 268 us here; 32 heads on each of
+// two, 174 and 261 us; 17 heads on one, 100 and 140 us.
 KvAttnPlan kv_attn_plan(const KvRef& kv, int32_t B, int32_t H, int32_t n_kv_heads, int32_t d, int64_t max_len,
                         int32_t window, bool invariant) {
   KvAttnPlan p{};

@@ -4,7 +4,7 @@
 //
 // From 17 heads on a key costs more products than mma.sync has time for while it
 // streams in (measured there: 64 heads on one KV head, 8 x 131072 slots of 128
-// dims, 270 us at 128 TFLOP/s, mma.sync's rate; the bytes alone take 82 us), so
+// dims, 268 us at 128 TFLOP/s, mma.sync's rate; the bytes alone take 82 us), so
 // the products go to tcgen05.  128 keys are the M side, up to 64 heads the N side:
 //   S^T [128 keys x 64 heads]  = K [keys x dims] . Q^T         (A, B K-major)
 //   O^T [dims x 64 heads]     += V^T [dims x keys] . P^T       (A, B MN-major)
@@ -23,12 +23,14 @@
 //   warp 9     page ids and TMA
 //   warp 10    the next segment's query heads, into the swizzled tile
 // Waits are bounded; a wait that runs out is recorded and ends the CTA's work.
-// What bounds it: the issuing thread.  Stamps of a long run (debug copy) give per
-// 128-key tile about 900 cycles for the eight products of S^T, 1400 for those of
-// P V with their three commits, and 500 of waits, about 1.5 us; the softmax warps
-// need 2000 of those cycles and wait for the rest.  Four groups of half the heads
-// left that as it is (64 heads over 8 x 131072 slots: 116 and 115 us; 32 heads on
-// each of two: 183 and 191).
+// What paces it: the issuing thread (64 heads over 8 x 131072 slots: 107 us, 5.0
+// TB/s and 321 TFLOP/s; 32 heads on each of two: 174 us).  Stamps of a long run,
+// of a copy with one commit more a tile, gave per 128-key tile about 900 cycles for the
+// eight products of S^T, 1400 for those of P V with their commits, and 500 of
+// waits; the softmax warps needed 2000 of those cycles and waited for the rest.
+// The products themselves need less (96 KB of operands a tile, 770 cycles at 128
+// bytes a cycle), so this is the issuing code's pace, not the chip's.  Four softmax
+// groups of half the heads left it as it was (116 and 115 us at the time).
 #include "kv_attention.cuh"
 
 namespace csa {

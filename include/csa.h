@@ -539,11 +539,16 @@ csa_status_t hca_attn(const csa_bf16* q, const csa_cache_t* kv_comp, const csa_b
  *               s % page_size of page page_table[b*max_pages + s/page_size];
  *               NULL: contiguous, sequence b is page b and max_pages is taken as 1
  *   head_dim    a multiple of 8 in [8, 256]; page_size >= 1;
- *               max_pages*page_size < 2^31
+ *               max_pages*page_size <= 2^30, n_pages < 2^31, n_kv_heads <= 65535
  * A sequence with n tokens in the cache uses slots 0 .. n-1 (lens[b] = n).
  * Calls that write a cache (append, evict) need every written slot to have a
  * place of its own: strides that do not overlap and no page that two of the
- * batch's sequences share there.
+ * batch's sequences share there.  (A cache whose k and v are the same memory is
+ * read and evicted from by these calls; csa_kv_append refuses it.)
+ * A call takes up to 65535 sequences, csa_kv_attn_decode up to 2^27 sequences
+ * times query heads, csa_kv_evict up to 2^27 sequences times KV heads and a
+ * budget of 2^24.  A workspace serves one call at a time: calls that may run at
+ * once (two streams, two threads, two captured graphs) need one each.
  */
 typedef enum { CSA_KV_BF16 = 0, CSA_KV_FP16 = 1 } csa_kv_dtype_t;
 
