@@ -23,9 +23,8 @@
 //     columns matter).  Up to 16 heads (8 of more than 128 dims), the CTA's four
 //     warps take the tile's keys apart, each with a ring of its own (no block
 //     barrier in the loop); more heads put 2 and 4 warps side by side on the
-//     same keys.  Rows come as
-//     TMA boxes of 16 rows (or, where 16 slots may lie on several pages, by
-//     cp.async), page ids one step ahead of them.
+//     same keys.  Rows come as TMA boxes of 16 rows (or, where 16 slots may lie
+//     on several pages, by cp.async), page ids one step ahead of them.
 //   * Softmax with a running maximum in base 2 and fp32; probabilities rounded
 //     to the cache's type for P V (as every 16-bit tensor-core product needs; in
 //     fp16 times 2^14), their sum taken before that rounding.

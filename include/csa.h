@@ -122,7 +122,7 @@ csa_status_t csa_set_attention_kernel(int32_t choice);
  * log-sum-exp are then bit-identical whether it is decoded alone or in any
  * batch, at some cost in speed for small batches.  csa_kv_attn_decode cuts a
  * sequence's slots in the same way; its output, log-sum-exp and weights depend
- * neither on the batch nor on max_len then.  The decode and HCA
+ * neither on the batch nor on max_len then.  The decode, HCA and key-value
  * workspace-size queries account for the mode in force when they are called.
  * DeepSeek-V4 infrastructure notes, "batch invariance": split-KV decoding
  * otherwise makes the accumulation order, and so the bits, depend on the
